@@ -33,6 +33,9 @@ SPA_K_INDEX_APPEND, SPA_K_SELECT, SPA_K_ATTEND, SPA_K_COMBINE, SPA_K_KV_APPEND, 
 SPA_K_COUNT = 7
 SPA_CP_STATS, SPA_CP_MASS, SPA_CP_ROUND2, SPA_CP_ROUND3, SPA_CP_ATTEND = range(5)
 SPA_CP_NBUF = 6
+SPA_ROPE_HALF, SPA_ROPE_INTERLEAVED = range(2)
+SPA_ROPE_PLAIN, SPA_ROPE_LINEAR, SPA_ROPE_BASE, SPA_ROPE_BANDS, SPA_ROPE_RAMP = range(5)
+SPA_PAGE_INT4, SPA_PAGE_BF16 = range(2)
 
 
 class SpaError(RuntimeError):
@@ -85,6 +88,34 @@ class spa_cp_args(ctypes.Structure):
     ]
 
 
+class spa_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int),
+        ("layout", ctypes.c_int),
+        ("scaling", ctypes.c_int),
+        ("theta", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("orig_ctx", ctypes.c_int64),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
+class spa_paged_config(ctypes.Structure):
+    _fields_ = [
+        ("max_batch", ctypes.c_int),
+        ("n_q_heads", ctypes.c_int),
+        ("n_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("kv_dtype", ctypes.c_int),
+        ("page_format", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("n_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+    ]
+
+
 _vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _SIGS = {
     "spa_create": (_i, [ctypes.POINTER(_vp), ctypes.POINTER(spa_config)]),
@@ -117,6 +148,17 @@ _SIGS = {
     "spa_profile_read": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]),
     "spa_kernel_name": (ctypes.c_char_p, [_i]),
     "spa_launch_count": (_i, [_vp, ctypes.POINTER(ctypes.c_int64)]),
+    "spa_rope_create": (_i, [ctypes.POINTER(_vp), ctypes.POINTER(spa_rope_config)]),
+    "spa_rope_destroy": (_i, [_vp]),
+    "spa_rope_inv_freq": (_i, [_vp, _vp, _i]),
+    "spa_rope_apply": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "spa_paged_page_bytes": (_i, [ctypes.POINTER(spa_paged_config), ctypes.POINTER(ctypes.c_size_t)]),
+    "spa_paged_create": (_i, [ctypes.POINTER(_vp), ctypes.POINTER(spa_paged_config), _vp]),
+    "spa_paged_destroy": (_i, [_vp]),
+    "spa_paged_status": (_i, [_vp, _vp]),
+    "spa_kv_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+    "spa_kv_read_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "spa_attend_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i64, _vp, _i, _i, _vp, _vp, _i64, _vp, _vp, _vp]),
     "spa_select_noalloc": (_i, [_vp, _i, _i, _i, _f, _i64, _vp, _vp, _vp, _vp, _i, _i64, _f, _i, _i, _vp, _vp,
                                 _vp]),
 }
@@ -375,3 +417,108 @@ def spa_select_noalloc(P_q, n_q_heads: int, n_kv_heads: int, kv_dtype: int, idx_
     _check(load().spa_select_noalloc(_ptr(P_q), n_q_heads, n_kv_heads, kv_dtype, idx_scale, max_ctx, _ptr(q_pre),
                                      _ptr(idx_cache), _host_u8(head_mask), _ptr(seq_lens), B, max_seq_len, p,
                                      n_sink, window, _ptr(sel_idx), _ptr(sel_count), _stream(stream)))
+
+
+# ---- rotary positions and the paged cache
+
+def _dev(x) -> Optional[int]:
+    """_ptr of a tensor that a kernel reads: a host tensor, or one of another device than the
+    current one, is refused (its address would fault on the GPU)."""
+    if x is None or isinstance(x, int):
+        return x
+    d = x.get_device()
+    if d < 0:
+        raise ValueError("expected a CUDA tensor, got one in host memory")
+    import torch
+    if d != torch.cuda.current_device():
+        raise ValueError(f"tensor on device {d}, the current device is {torch.cuda.current_device()}")
+    return x.data_ptr()
+
+
+def _strides(s):
+    return None if s is None else (ctypes.c_int64 * 3)(*s)
+
+
+def make_rope_config(*, rot_dim: int = 128, layout: int = SPA_ROPE_HALF, theta: float = 500000.0,
+                     scaling: int = SPA_ROPE_PLAIN, factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                     orig_ctx: int = 0, magnitude: float = 1.0) -> spa_rope_config:
+    return spa_rope_config(rot_dim=rot_dim, layout=layout, scaling=scaling, theta=theta, factor=factor, low=low,
+                           high=high, orig_ctx=orig_ctx, magnitude=magnitude)
+
+
+def spa_rope_create(cfg: spa_rope_config) -> int:
+    r = ctypes.c_void_p(None)
+    _check(load().spa_rope_create(ctypes.byref(r), ctypes.byref(cfg)))
+    return r.value
+
+
+def spa_rope_destroy(r) -> None:
+    _check(load().spa_rope_destroy(r))
+
+
+def spa_rope_inv_freq(r, n: int) -> Tuple[float, ...]:
+    """The n = rot_dim / 2 inverse frequencies in use."""
+    f = (ctypes.c_double * max(n, 1))()
+    _check(load().spa_rope_inv_freq(r, f, n))
+    return tuple(f)[:n]
+
+
+def spa_rope_apply(r, x, y, B: int, T: int, n_heads: int, head_dim: int, dtype: int, start_pos=None, positions=None,
+                   x_strides=None, y_strides=None, transpose: bool = False, stream=None) -> None:
+    """Strides are (batch, token, head) in elements; None is dense [B][n_heads][T][head_dim]."""
+    _check(load().spa_rope_apply(r, _dev(x), _strides(x_strides), _dev(y), _strides(y_strides), _dev(start_pos),
+                                 _dev(positions), B, T, n_heads, head_dim, dtype, 1 if transpose else 0,
+                                 _stream(stream)))
+
+
+def make_paged_config(*, max_batch: int, n_q_heads: int, n_kv_heads: int, kv_dtype: int, page_format: int,
+                      page_size: int, n_pages: int, max_pages: int, head_dim: int = 128) -> spa_paged_config:
+    return spa_paged_config(max_batch=max_batch, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
+                            kv_dtype=kv_dtype, page_format=page_format, page_size=page_size, n_pages=n_pages,
+                            max_pages=max_pages)
+
+
+def spa_paged_page_bytes(cfg: spa_paged_config) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().spa_paged_page_bytes(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def spa_paged_create(cfg: spa_paged_config, rope=None) -> int:
+    h = ctypes.c_void_p(None)
+    _check(load().spa_paged_create(ctypes.byref(h), ctypes.byref(cfg), rope))
+    return h.value
+
+
+def spa_paged_destroy(h) -> None:
+    _check(load().spa_paged_destroy(h))
+
+
+def spa_paged_status(h, stream=None) -> None:
+    _check(load().spa_paged_status(h, _stream(stream)))
+
+
+def spa_kv_append_paged(h, k_pre, v_new, start_pos, B: int, T: int, block_table, pages, n_new=None, k_strides=None,
+                        v_strides=None, stream=None) -> None:
+    """Strides are (batch, token, head) in elements; None is dense [B][Hkv][T][128]."""
+    _check(load().spa_kv_append_paged(h, _dev(k_pre), _strides(k_strides), _dev(v_new), _strides(v_strides),
+                                      _dev(start_pos), _dev(n_new), B, T, _dev(block_table), _dev(pages),
+                                      _stream(stream)))
+
+
+def spa_kv_read_paged(h, pages, block_table, start_pos, B: int, T: int, k_rows, v_rows, n_rows=None, k_strides=None,
+                      v_strides=None, stream=None) -> None:
+    """Strides are (batch, token, head) in elements; None is dense [B][Hkv][T][128]."""
+    _check(load().spa_kv_read_paged(h, _dev(pages), _dev(block_table), _dev(start_pos), _dev(n_rows), B, T,
+                                    _dev(k_rows), _strides(k_strides), _dev(v_rows), _strides(v_strides),
+                                    _stream(stream)))
+
+
+def spa_attend_paged(h, q_pre, pages, block_table, seq_lens, B: int, max_seq_len: int, out, head_mask=None,
+                     n_sink: int = 0, window: int = 0, sel_idx=None, sel_count=None, sel_stride: int = 0, lse=None,
+                     stream=None) -> None:
+    """head_mask: None (every head attends every row), or the host mask [Hkv] (bytes, list or tensor)."""
+    mask = None if head_mask is None else head_mask if isinstance(head_mask, bytes) else _host_u8(head_mask)
+    _check(load().spa_attend_paged(h, _dev(q_pre), _dev(pages), _dev(block_table), _dev(seq_lens), B, max_seq_len,
+                                   mask, n_sink, window, _dev(sel_idx), _dev(sel_count), sel_stride, _dev(out),
+                                   _dev(lse), _stream(stream)))

@@ -408,6 +408,152 @@ SPA_API spa_status spa_head_effective_ranks(const float* W_Q, const float* W_K, 
                       int d_model, int n_retrieval, void* workspace, size_t workspace_bytes, double* er_q,
                       double* er_kv, uint8_t* head_mask, double* sigma_opt, spa_stream stream);
 
+/* ---- rotary positions ----
+ *
+ * The library rotates the queries of its own steps; these calls rotate anything else (the
+ * keys a caller writes into k_cache, above all).  A rotation belongs to no device: it is a host
+ * table that every call passes to its kernel.
+ *   y = m R(pos) x on the first rot_dim dims of a head, y = x on the others;
+ *   R turns pair i by pos * f_i: (u, v) -> (u cos - v sin, u sin + v cos), with the pair
+ *     (i, i + rot_dim / 2)   SPA_ROPE_HALF
+ *     (2i, 2i + 1)           SPA_ROPE_INTERLEAVED
+ *   f_i = theta^(-2i / rot_dim), changed for contexts longer than the trained one by
+ *     SPA_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *     SPA_ROPE_BASE    theta * factor^(rot_dim / (rot_dim - 2)) in theta's place
+ *     SPA_ROPE_BANDS   f_i (k + (1 - k) / factor), k = (orig_ctx f_i / 2 pi - low) / (high - low) in [0, 1]:
+ *                      pairs of more than `high` turns over the trained context keep their frequency
+ *     SPA_ROPE_RAMP    the same blend with k = 1 - (i - a) / (b - a) in [0, 1], a and b the pair numbers
+ *                      floor(n(high)), ceil(n(low)) kept in [0, rot_dim - 1] (b = a + 0.001 where they meet),
+ *                      n(turns) = rot_dim ln(orig_ctx / (2 pi turns)) / (2 ln theta)
+ * Angles are taken in 64 bits; a position is exact up to 2^50 in magnitude (angles to 2^-52 of theirs). */
+#define SPA_ROPE_HALF 0
+#define SPA_ROPE_INTERLEAVED 1
+#define SPA_ROPE_PLAIN 0
+#define SPA_ROPE_LINEAR 1
+#define SPA_ROPE_BASE 2
+#define SPA_ROPE_BANDS 3
+#define SPA_ROPE_RAMP 4
+typedef struct spa_rope spa_rope;
+typedef struct {
+  int rot_dim;       /* even, 2..512 */
+  int layout;        /* SPA_ROPE_HALF or SPA_ROPE_INTERLEAVED */
+  int scaling;       /* SPA_ROPE_PLAIN .. SPA_ROPE_RAMP */
+  double theta;      /* > 0 (SPA_ROPE_RAMP: > 1) */
+  double factor;     /* > 0; unused by SPA_ROPE_PLAIN */
+  double low, high;  /* 0 < low < high: turns over orig_ctx (SPA_ROPE_BANDS, SPA_ROPE_RAMP) */
+  int64_t orig_ctx;  /* trained context (SPA_ROPE_BANDS, SPA_ROPE_RAMP) */
+  double magnitude;  /* m; 0 selects 1 */
+} spa_rope_config;
+
+/* Host only.  On failure *out is NULL.  NULL may be destroyed. */
+SPA_API spa_status spa_rope_create(spa_rope** out, const spa_rope_config* cfg);
+SPA_API spa_status spa_rope_destroy(spa_rope* r);
+/* The frequencies f_i in use, i < n = rot_dim / 2, to HOST memory. */
+SPA_API spa_status spa_rope_inv_freq(const spa_rope* r, double* inv_freq, int n);
+
+/* Rotates x [B][T][n_heads][head_dim] into y (SPA_BF16 or SPA_F32; float32 arithmetic, rounded once).
+ *   x_strides, y_strides  HOST int64 [3], elements: (batch, token, head); the dims of a head are contiguous.
+ *                         NULL: dense [B][n_heads][T][head_dim].  x's may be 0 or negative (a broadcast
+ *                         input); no two elements of y may share a place
+ *   start_pos             device int64 [B]: token t is at start_pos[b] + t, or
+ *   positions             device int64 [B][T]: each token's own; exactly one of the two is given
+ *   transpose             non-zero: m R(pos)^T, the gradient of x for a gradient in x's place
+ * y may be x (same strides); otherwise they may not overlap.  16-byte vectors where pointers, strides,
+ * rot_dim and head_dim allow them, narrower ones elsewhere.  Runs on the current device.
+ * Errors: SPA_ERR_INVALID_ARG for NULL or misaligned pointers, both or neither of the positions, B, T or
+ * n_heads < 1, head_dim outside [rot_dim, 65536]. */
+SPA_API spa_status spa_rope_apply(const spa_rope* r, const void* x, const int64_t* x_strides, void* y,
+                      const int64_t* y_strides, const int64_t* start_pos, const int64_t* positions, int B, int T,
+                      int n_heads, int head_dim, int dtype, int transpose, spa_stream stream);
+
+/* ---- paged KV cache, in 4 bits or bf16 ----
+ *
+ * A pool of pages of page_size tokens; page block_table[b][t / page_size] holds position t of
+ * sequence b for every KV head (spa_kv_append_paged writes it, spa_attend_paged and spa_kv_read_paged
+ * read it).  Keys are stored rotated.  Layout of the pool: bytes
+ *   pages[n_pages][n_kv_heads][page_size / 16][block],  block = 16 tokens of one KV head:
+ *   SPA_PAGE_INT4 (2304 bytes): K codes [16][64], V codes [16][64], bf16 scales [16][8] (4 of K, 4 of V);
+ *     dim d of a row is nibble d (low nibble first) and stands for scale * (nibble - 8); the scale is that of
+ *     group (d / 8) % 4 for K, (d / 4) % 4 for V.  Written: scale = bf16(largest magnitude of the group / 7),
+ *     nibble = clamp(round_half_even(x / scale), -7, 7) + 8; a group whose magnitudes are all below 2^-110 is
+ *     stored as zeros, one that holds an infinity or NaN with scale NaN (all its values read back as NaN).
+ *     144 bytes a row pair, against 512 in bf16
+ *   SPA_PAGE_BF16 (8192 bytes): K [16][128], V [16][128] bf16; the 16-byte piece c of row r lies at piece c ^ (r % 8)
+ * Sequences may share pages that are only read.
+ *
+ * The handle owns a workspace (split states of the attention, a status word) on the device current at
+ * create; every call needs that device to be current.  Calls only enqueue work on `stream` and may be captured
+ * in CUDA graphs.  Two spa_attend_paged calls (or graphs that hold one) on the same handle must not run at the
+ * same time: use a handle each.  Lengths, positions, counts and block_table entries are checked on the device: an
+ * out-of-range one is clamped or its rows skipped, and spa_paged_status reports it. */
+#define SPA_PAGE_INT4 0
+#define SPA_PAGE_BF16 1
+typedef struct spa_paged spa_paged;
+typedef struct {
+  int max_batch;     /* largest B a call may pass; max_batch * n_kv_heads <= 4096 */
+  int n_q_heads;     /* Hq; Hq / Hkv in 1..8 */
+  int n_kv_heads;    /* Hkv <= 64 */
+  int head_dim;      /* must be 128 */
+  int kv_dtype;      /* SPA_BF16 or SPA_F32: type of queries and of new or read-back rows */
+  int page_format;   /* SPA_PAGE_INT4 or SPA_PAGE_BF16 */
+  int page_size;     /* tokens of a page: a multiple of 16, at most 65536 */
+  int n_pages;       /* pages of the pool */
+  int max_pages;     /* columns of block_table; max_pages * page_size <= 2^24 tokens a sequence */
+} spa_paged_config;
+
+/* Bytes of one page (every KV head): the pool has n_pages times as many.  Host only. */
+SPA_API spa_status spa_paged_page_bytes(const spa_paged_config* cfg, size_t* bytes);
+/* `rope` turns the appended keys and the queries (rot_dim <= 128); its table is copied.  NULL: no
+ * rotation (both come rotated).  Synchronous.  On failure *out is NULL. */
+SPA_API spa_status spa_paged_create(spa_paged** out, const spa_paged_config* cfg, const spa_rope* rope);
+/* Frees the workspace (synchronises the device first).  NULL is accepted. */
+SPA_API spa_status spa_paged_destroy(spa_paged* h);
+/* Synchronises `stream`, reads and clears the status word: SPA_OK, SPA_ERR_DEVICE_RANGE or
+ * SPA_ERR_DEVICE_TIMEOUT. */
+SPA_API spa_status spa_paged_status(spa_paged* h, spa_stream stream);
+
+/* Rotates, rounds and stores T new tokens of every (sequence, KV head) at positions
+ * start_pos[b] + t, t < n_new[b].
+ *   k_pre, v_new  device kv_dtype [B][T][n_kv_heads][128] by HOST strides (batch, token, head) in elements,
+ *                 multiples of 16 bytes (the rows of a fused projection need no copy); NULL: dense [B][n_kv_heads][T][128]
+ *   start_pos     device int64 [B]
+ *   n_new_opt     NULL (T of every sequence), or device int64 [B] in [0, T]: a padded batch
+ *   block_table   device int32 [B][max_pages]; only entries of written positions are read
+ *   pages         device, 16-byte aligned; nothing but the new rows is written
+ * A page that the call writes must not be another sequence's too. */
+SPA_API spa_status spa_kv_append_paged(spa_paged* h, const void* k_pre, const int64_t* k_strides, const void* v_new,
+                      const int64_t* v_strides, const int64_t* start_pos, const int64_t* n_new_opt, int B, int T,
+                      const int32_t* block_table, void* pages, spa_stream stream);
+
+/* Reads positions start_pos[b] + t, t < n_rows[b] (NULL: T), as stored: rotated keys, and for
+ * SPA_PAGE_INT4 the values that the codes stand for, rounded to kv_dtype.  Into k_rows, v_rows
+ * [B][T][n_kv_heads][128] by HOST strides, as for the append (NULL: dense [B][n_kv_heads][T][128], which
+ * spa_prefill and spa_decode take as a cache of T rows when start_pos is 0).  Rows at and behind n_rows[b], and
+ * rows whose position or page is out of range, are left as they were. */
+SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int32_t* block_table,
+                      const int64_t* start_pos, const int64_t* n_rows_opt, int B, int T, void* k_rows,
+                      const int64_t* k_strides, void* v_rows, const int64_t* v_strides, spa_stream stream);
+
+/* Attention of one token a sequence over the pages, L = seq_lens[b] rows of it being stored:
+ *   out[b][h] = sum_{j in S} softmax_j(<m R(L-1) q_pre[b][h], K_j> / sqrt(128)) V_j
+ *   head_mask NULL:          S = [0, L) for every head
+ *   streaming head (0):      S = sinks and window, as in spa_decode
+ *   retrieval head (1):      S = [0, L), or with a selection: sinks, window and sel_idx[b][g][0 .. sel_count)
+ * (a selection as spa_select returns it: its list excludes sinks and window; a position listed twice counts twice).
+ *   q_pre      device kv_dtype [B][Hq][128]
+ *   seq_lens   device int64 [B], 0..max_seq_len; a sequence of length 0 gives zeros
+ *   max_seq_len  host bound; 0 = max_pages * page_size
+ *   head_mask_opt  HOST uint8 [Hkv]; n_sink, window >= 0, n_sink + window >= 1 (read only with a mask)
+ *   sel_idx_opt, sel_count_opt  device int32 [B][Hkv][sel_stride] and [B * Hkv]; both or neither
+ *   out        device float32 [B][Hq][128]; lse_opt NULL or device float32 [B][Hq]: log2 of the softmax
+ *              denominator (-infinity for zeros), as spa_cp_combine takes it
+ * Queries and probabilities are kept to about 17 bits for the tensor cores, sums in float32; the result does
+ * not depend on timing.  Masked rows contribute nothing, whatever their bytes. */
+SPA_API spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, const int32_t* block_table,
+                      const int64_t* seq_lens, int B, int64_t max_seq_len, const uint8_t* head_mask_opt, int n_sink,
+                      int window, const int32_t* sel_idx_opt, const int32_t* sel_count_opt, int64_t sel_stride,
+                      float* out, float* lse_opt, spa_stream stream);
+
 /*
  * Synchronise `stream`, then read and clear the handle's device status word.
  * Returns SPA_ERR_DEVICE_RANGE (with the offending field named in
