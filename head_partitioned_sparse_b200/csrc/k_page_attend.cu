@@ -4,39 +4,55 @@
 // head attends: every row, or sinks and window, or sinks, window and a selected list.
 //
 // Work layout.  The attended rows of all (sequence, KV head) slices are cut into units of 16
-// rows: whole 16-token blocks of the pages (edges masked), or 16 listed rows.  Every CTA (one an
-// SM) takes an equal contiguous share of the units, one piece per slice it touches, and its warps the units
-// of a piece in turn.  Each warp streams its units through its own ring in shared memory: a
-// block is one bulk copy (2304 bytes in 4 bits, K, V and scales together), a listed unit is
-// gathered by 16-byte asynchronous copies.  The list position of the unit after next and the block table
-// entry of the next one are loaded ahead, so no copy waits for an index.  Warps keep their own
-// running maximum and sum, merged by a tree at the end of a piece; the last CTA to finish a
-// slice (a ticket) merges the CTAs' states in order, so the result does not depend on timing.
+// rows: whole 16-token blocks of the pages (edges masked), or 16 listed rows; U consecutive units of a
+// slice are an item.  Every CTA (one an SM) takes an equal contiguous share of the items, and its
+// warps take them in turn, each through a ring of its own in shared memory.  A warp looks up 32 units at a
+// time, a lane each (slice, page, byte offset, row mask), so the search, the division and the block
+// table cost 1/32 a unit, and those lanes start the copies: a block is one bulk copy (2304 bytes in 4
+// bits: K, V and scales together).  Listed units are gathered by 16-byte asynchronous copies, their
+// positions loaded two items ahead, their pages one.
+// (Two producer warps for the whole CTA were measured 1.8 times slower: one lane's waits and copies in turn.)
+// Warps keep their own running maximum and sum, merged by a tree at the end of a slice's piece;
+// the last CTA to finish a slice (a ticket) merges the CTAs' states in order, so the result does
+// not depend on timing.
 //
-// Matrix mapping (mma.sync m16n8k16, M = 8 heads as bf16 high parts over 8 rows of bf16 residuals, so scores and
-// sums keep about 17 bits):
-//   4 bits: a code word (8 nibbles) becomes four bf16 pairs of 128 + n, (nibble j, nibble j + 4), less 136.
+// Matrix mapping (mma.sync m16n8k16, float32 sums).  The 16 rows of the operand hold the group's heads more
+// than once, as a high part and residuals, so that no bits of queries and probabilities are lost:
+//   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
+//     to a maximum of 2^10 a head; probabilities are 2^11 times their value and value scales at most 2^4
+//     by the largest scale the warp has met (a power of two, moved like the running maximum), so
+//     float16's range holds both.  A code word (8 nibbles) becomes four float16 pairs, (nibble j,
+//     nibble j + 4), by a mask each: small integers under a zero exponent are subnormals.
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
-//     are summed by themselves and scaled once a (row, group), not once an element.
+//     are summed by themselves (starting at -8 times the sum of the queries, which centres
+//     the codes) and scaled once a (row, group), not once an element.
 //     Values: the halves of two rows' words are merged by one byte permute into (row, row + 1)
-//     pairs; column tile t holds dims 16 n + t, all of scale group t / 4, whose scales go into the
-//     probabilities (four sets of them).
-//   bf16: matrix loads from the swizzled rows.
+//     pairs and centred by an addition (their sums run over the whole context: no cancellation is
+//     put into them); column tile t holds dims 16 n + t, all of scale group t / 4, whose
+//     scales go into the probabilities (four sets of them, in packed float16 with exact residuals).
+//   bf16: three bf16 parts (24 bits).  Up to 4 heads they share one operand (high rows 0-3, middle rows 4-7, low
+//     rows 8-11; lanes 16 apart add up), more heads take a second product for the low part.
+//     Rows come by matrix loads from the swizzled block.
 //
 // Masked rows: their score is -infinity and their value scale (bf16: their value) 0, whatever the page holds there.
+#include <climits>
+
+#include <cuda_fp16.h>
+
 #include "spa_paged.cuh"
 
 namespace spa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 8;
 constexpr float kNoMax = -1e30f;        // running maximum before the first row
-constexpr unsigned kWaitTries = 1u << 22;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, unsigned n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar, unsigned n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -45,17 +61,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(bar), "l"(pol)
       : "memory");
 }
+__device__ __forceinline__ bool mbar_try(uint32_t bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase to end, for two seconds at most.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity) {
-  for (unsigned i = 0; i < kWaitTries; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try(bar, parity))
+    if (now_ns() - t0 > 2000000000ull) return false;
+  return true;
 }
 __device__ __forceinline__ uint64_t l2_evict_first() {
   uint64_t p;
@@ -65,12 +91,25 @@ __device__ __forceinline__ uint64_t l2_evict_first() {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = A B + c, c.x in the upper rows and c.y in the lower ones.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, float2 c) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%11,%11};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y));
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -82,6 +121,12 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
+// A read that stays where it is: 32 registers of query operands would not fit beside the sums.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -91,18 +136,47 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// (nibble j, nibble j + 4) of w as a bf16 pair of n - 8: 128 + n by its bits, less 136 (exact).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
-  uint32_t u = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-  __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&u);
-  v = __hsub2(v, __nv_bfloat162(__float2bfloat16_rn(136.f), __float2bfloat16_rn(136.f)));
-  return *reinterpret_cast<uint32_t*>(&v);
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w as float16 pairs of n 2^-24, the second and fourth 16 times that.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t v = w >> 8;
+  r[0] = w & 0x000f000fu;
+  r[1] = w & 0x00f000f0u;
+  r[2] = v & 0x000f000fu;
+  r[3] = v & 0x00f000f0u;
 }
-// The bf16 high parts and residuals of a pair.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+// The same of n - 8 (exact).
+__device__ __forceinline__ void centred_pairs(uint32_t w, uint32_t (&r)[4]) {
+  code_pairs(w, r);
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[0]) : "r"(0x80088008u));
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[1]) : "r"(0x80808080u));
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[2]) : "r"(0x80088008u));
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[3]) : "r"(0x80808080u));
+}
+constexpr float kCodeUnit = 16777216.f;   // 2^24: what a code of 1 stands for in float16, inverted
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+// Float16 high parts and residuals of a pair.
+__device__ __forceinline__ void split_f16(float x, float y, __half2& hi, __half2& lo) {
+  hi = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(hi);
+  lo = __floats2half2_rn(x - f.x, y - f.y);
+}
+// The three bf16 parts of a pair.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack2(x, y);
-  lo = pack2(x - bf16_lo(hi), y - bf16_hi(hi));
+  x -= bf16_lo(hi);
+  y -= bf16_hi(hi);
+  mid = pack2(x, y);
+  lo = pack2(x - bf16_lo(mid), y - bf16_hi(mid));
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+constexpr float kProbExp = 11.f;         // 4 bits: probabilities are 2^11 times their value
+constexpr float kScaleTop = 16.f;        // 4 bits: value scales in float16, at most this
+constexpr unsigned kScaleLow = 0x0d80u;  // bf16 2^-100: the least bound of the value scales
 
 // Rows of one slice: blocks [0, nb0) (sinks), blocks [b1, b1 + nb1) (window, or every block), then cnt listed rows.
 struct Slice {
@@ -129,41 +203,53 @@ __device__ __forceinline__ Slice make_slice(const PagedAttendArgs& A, int g, int
   return S;
 }
 
-// A unit on its way to the ring: what has been loaded of it so far.
+// A unit, held by the lane that looked it up.
 struct Unit {
-  int s;        // slice, -1: none
-  int list;     // listed rows (else one block)
-  int pos;      // lane l < 16: position of row l (block: of row 0)
-  bool ok;      // lane l < 16: row l is attended
-  int id;       // page of pos
+  long long off;   // block: byte offset in the pool; list: index of its first entry
+  unsigned info;   // attended rows (16 bits), kList
+  int s;           // slice
 };
+// Listed rows on their way.
+struct Rows {
+  int pos, id, s;   // lane l < 16: position of row l (-1: not attended or not listed) and its page; the slice
+};
+constexpr unsigned kList = 0x10000u;
 
-template <int FMT, int S>
-__global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAttendArgs A, const __grid_constant__ RopeTab128 tab) {
+// W warps, items of U units (4 bits 2, bf16 1), S ring slots a warp; WIDE: more than 4 heads a group (bf16 only, see the matrix mapping); LISTED: a
+// selection is given.
+template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
+__global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArgs A, const __grid_constant__ RopeTab128 tab) {
+  constexpr bool kF16 = FMT == kPageInt4;
   constexpr int kBlk = FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
+  constexpr int kItems = 32 / U;   // items that 32 lanes look up
+  static_assert(U == (kF16 ? 2 : 1), "items of each format");
   extern __shared__ __align__(128) unsigned char smem[];
-  unsigned char* const ring = smem;                                              // [8][S][kBlk]
-  float* const mbuf = reinterpret_cast<float*>(smem + (size_t)kWarps * S * kBlk);   // [4][8][kPartStride]
-  float* const cbuf = mbuf + 4 * kMaxGroup * kPartStride;                        // [8][kPartStride]
-  float* const qs = cbuf + kWarps * kPartStride;                                 // [8][128]
+  unsigned char* const ring = smem;                                              // [W][S][U][kBlk]
+  float* const mbuf = reinterpret_cast<float*>(smem + (size_t)W * S * U * kBlk);     // [(W + 1) / 2][8][kPartStride]
+  float* const cbuf = mbuf + (W + 1) / 2 * kMaxGroup * kPartStride;              // [max(W, 8)][kPartStride]
+  float* const qs = cbuf + (W > kMaxGroup ? W : kMaxGroup) * kPartStride;        // [8][128]
   long long* const rpre = reinterpret_cast<long long*>(qs + kMaxGroup * kHeadDim);  // [n_slices + 1]
   int2* const sinfo = reinterpret_cast<int2*>(rpre + A.n_slices + 1);            // [n_slices] (L, listed rows)
-  __shared__ __align__(8) unsigned long long bars[kWarps * S];
-  __shared__ unsigned vmask[kWarps * S];   // attended rows of a ring slot; bit 16: gathered
-  __shared__ long long shl[kWarps];
+  __shared__ __align__(8) unsigned long long full[W * S];
+  __shared__ unsigned vmask[W * S * U];   // attended rows of a slot's units; bit 16: gathered
+  __shared__ long long shl[W];
   __shared__ int s_merge;
+  __shared__ uint4 qf[kF16 ? 8 * 32 : 1];      // 4 bits: query operands, a lane's 16 bytes of each k-step
+  __shared__ float2 q8[kF16 ? 4 * 8 : 1];      // 4 bits: -8 times a scale group's sum of queries (high, residual), each head
+  __shared__ __align__(16) float kscale[kF16 ? 4 * W * 32 : 4];   // 4 bits, of the item in hand: scales of K, by group and row
+  __shared__ uint4 vscale[kF16 ? W * 16 : 1];  // and of V in float16, (row, row + 1) pairs of each group
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, t4 = lane & 3;
   const int NS = A.n_slices, Hkv = A.pool.Hkv, G = A.G;
 
-  if (tid < kWarps * S) mbar_init(smem_u32(&bars[tid]), 1);
+  if (tid < W * S) mbar_init(smem_u32(&full[tid]), U);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-  // ---- unit prefix over slices
+  // ---- item prefix over slices
   {
     long long carry = 0;
-    for (int base = 0; base < NS; base += kWarps * 32) {
+    for (int base = 0; base < NS; base += W * 32) {
       const int s = base + tid;
       long long n = 0;
       if (s < NS) {
@@ -182,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
           }
         }
         sinfo[s] = make_int2((int)L, cnt);
-        n = units_of(make_slice(A, g, (int)L, cnt));
+        n = (units_of(make_slice(A, g, (int)L, cnt)) + U - 1) / U;
       }
       long long v = n;
 #pragma unroll
@@ -194,7 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
       __syncthreads();
       long long before = carry, total = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const long long x = shl[w];
         if (w < warp) before += x;
         total += x;
@@ -211,11 +297,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
   for (int s = blockIdx.x; s < NS; s += gridDim.x) {
     if (rpre[s + 1] != rpre[s]) continue;
     const size_t h0 = (size_t)(s / Hkv) * A.Hq + (size_t)(s % Hkv) * G;
-    for (int i = tid; i < G * kHeadDim; i += kWarps * 32) A.out[h0 * kHeadDim + i] = 0.f;
+    for (int i = tid; i < G * kHeadDim; i += W * 32) A.out[h0 * kHeadDim + i] = 0.f;
     if (A.lse && tid < G) A.lse[h0 + tid] = -INFINITY;
   }
-  // every active CTA has at least one unit a warp
-  const long long want = (T + kWarps - 1) / kWarps;
+  // every active CTA has at least one item a warp
+  const long long want = (T + W - 1) / W;
   const int nb = (long long)gridDim.x < want ? (int)gridDim.x : (int)want;
   if ((int)blockIdx.x >= nb) return;
   const long long r_lo = (long long)blockIdx.x * T / nb, r_hi = (long long)(blockIdx.x + 1) * T / nb;
@@ -230,104 +316,132 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
     return lo;
   };
   const int s_first = slice_of(r_lo), s_last = slice_of(r_hi - 1);
-  // units of slice s in this CTA's share
-  auto piece = [&](int s, int& u0, int& n) {
-    const long long a = max(r_lo, rpre[s]), e = min(r_hi, rpre[s + 1]);
-    u0 = (int)(a - rpre[s]);
-    n = e > a ? (int)(e - a) : 0;
-  };
-
-  unsigned char* const myring = ring + (size_t)warp * S * kBlk;
-  const uint32_t ring_a = smem_u32(myring), bar_a = smem_u32(&bars[warp * S]);
+  const uint32_t ring_a = smem_u32(ring) + warp * S * U * kBlk, bar_a = smem_u32(&full[warp * S]);
   const uint64_t pol = l2_evict_first();
 
-  // ---- the warp's unit cursor and the two units whose indices are being loaded
-  int cs = s_first, cu = warp, c_u0, c_n;
-  piece(cs, c_u0, c_n);
-  Slice cS = make_slice(A, cs % Hkv, sinfo[cs].x, sinfo[cs].y);
-  auto next_unit = [&]() {   // the cursor's unit with its position loads started; moves the cursor
-    Unit U;
-    U.s = -1;
-    U.list = 0;
-    U.pos = 0;
-    U.ok = false;
-    U.id = -1;
-    while (cu >= c_n) {
-      if (cs >= s_last) return U;
-      ++cs;
-      cu = warp;
-      piece(cs, c_u0, c_n);
-      cS = make_slice(A, cs % Hkv, sinfo[cs].x, sinfo[cs].y);
+  // ---- the warp's items r_lo + warp + W k, k < nk: lane i looks up unit i % U of item kItems j + i / U
+  const int nk = r_lo + warp < r_hi ? (int)((r_hi - r_lo - warp + W - 1) / W) : 0;
+  auto find = [&](int k) {
+    Unit X;
+    X.s = 0;
+    X.off = 0;
+    X.info = 0u;
+    k += lane / U;
+    if (k >= nk) return X;
+    const long long r = r_lo + warp + (long long)W * k;
+    const int s = slice_of(r);
+    const int b = s / Hkv, g = s - b * Hkv;
+    const Slice sl = make_slice(A, g, sinfo[s].x, sinfo[s].y);
+    const int u = (int)(r - rpre[s]) * U + lane % U;
+    X.s = s;
+    if (u >= units_of(sl)) return X;
+    if (LISTED && u >= sl.nb0 + sl.nb1) {
+      const int i = (u - sl.nb0 - sl.nb1) * 16;
+      X.off = (long long)s * A.list_stride + i;
+      X.info = kList | (0xffffu >> (16 - min(16, sl.cnt - i)));
+      return X;
     }
-    const int u = c_u0 + cu;
-    cu += kWarps;
-    U.s = cs;
-    if (u < cS.nb0 + cS.nb1) {
-      const int blk = u < cS.nb0 ? u : cS.b1 + (u - cS.nb0);
-      U.pos = blk * kBlockTok;
-      const int p = U.pos + lane;
-      U.ok = lane < kBlockTok && p < cS.L && (p < cS.n_s || p >= cS.w_lo);
+    const int blk = u < sl.nb0 ? u : sl.b1 + (u - sl.nb0);
+    const int p0 = blk * kBlockTok;
+    // rows [0, L), below n_s or at least w_lo
+    auto below = [&](int q) { return q <= p0 ? 0u : 0xffffu >> (16 - min(16, q - p0)); };
+    const unsigned rows = below(sl.L) & (below(sl.n_s) | ~below(sl.w_lo));
+    const unsigned pg = (unsigned)blk / (unsigned)A.pool.page_blocks, in = (unsigned)blk - pg * (unsigned)A.pool.page_blocks;
+    const int id = __ldg(A.pool.table + (size_t)b * A.pool.max_pages + pg);
+    if ((unsigned)id < (unsigned)A.pool.n_pages) {
+      X.off = ((long long)id * Hkv + g) * A.pool.head_bytes + (long long)in * kBlk;
+      X.info = rows;
     } else {
-      U.list = 1;
-      const int i = (u - cS.nb0 - cS.nb1) * 16 + lane;
-      U.ok = lane < 16 && i < cS.cnt;
-      if (U.ok) U.pos = __ldg(A.list + (size_t)cs * A.list_stride + i);
+      atomicOr(A.pool.err, kErrPage);
     }
-    return U;
+    return X;
   };
-  auto load_page = [&](Unit& U) {
-    if (U.s < 0) return;
-    if (U.list && U.ok && (U.pos < 0 || U.pos >= sinfo[U.s].x)) {
+  // `cur` holds the item to be issued; `nxt`, where it differs, the item two ahead of it (lists)
+  Unit cur = find(0), nxt = cur;
+  int ki = 0;   // the next item to issue
+  auto list_rows = [&](int k) {   // starts the loads of item k's positions
+    Rows R;
+    R.pos = R.id = -1;
+    R.s = 0;
+    if (k >= nk) return R;
+    const Unit& B = k / kItems == ki / kItems ? cur : nxt;
+    const int from = k % kItems * U + (U == 2 ? lane >> 4 : 0);
+    const unsigned info = __shfl_sync(kFull, B.info, from);
+    if (!__any_sync(kFull, info & kList)) return R;
+    const long long off = __shfl_sync(kFull, B.off, from);
+    R.s = __shfl_sync(kFull, B.s, from);
+    if (lane < 16 * U && (info & kList) && (info >> (lane & 15) & 1u)) {
+      R.pos = __ldg(A.list + off + (lane & 15));
+      if (R.pos < 0) R.pos = INT_MAX;   // refused with the positions past the end
+    }
+    return R;
+  };
+  auto list_pages = [&](Rows& R) {   // checks the positions, starts the loads of their pages
+    if (R.pos < 0) return;
+    if (R.pos >= sinfo[R.s].x) {
       atomicOr(A.pool.err, kErrList);
-      U.ok = false;
-      U.pos = 0;
+      R.pos = -1;
+      return;
     }
-    const int b = U.s / Hkv;
-    const unsigned pg = ((unsigned)U.pos / kBlockTok) / (unsigned)A.pool.page_blocks;
-    if (!U.list || U.ok) U.id = __ldg(A.pool.table + (size_t)b * A.pool.max_pages + pg);
+    const unsigned pg = ((unsigned)R.pos / kBlockTok) / (unsigned)A.pool.page_blocks;
+    R.id = __ldg(A.pool.table + (size_t)(R.s / Hkv) * A.pool.max_pages + pg);
   };
-  int issued = 0;          // ring slot of the next issue
+  Rows r0, r1;   // of items ki and ki + 1
+  if (LISTED) {
+    r0 = list_rows(0);
+    list_pages(r0);
+    r1 = list_rows(1);
+  }
+  int islot = 0;           // ring slot of item ki
   unsigned was_list = 0u;  // slots last written by gathers
-  auto issue = [&](const Unit& U) {
-    if (U.s >= 0) {
-      const bool page_ok = (unsigned)U.id < (unsigned)A.pool.n_pages;
-      if (!page_ok && (U.ok || (!U.list && lane == 0))) atomicOr(A.pool.err, kErrPage);
-      const unsigned m = __ballot_sync(kFull, U.ok && page_ok) & 0xffffu;
-      const int g = U.s % Hkv;
-      const unsigned blkno = (unsigned)U.pos / kBlockTok;
-      const unsigned in = blkno % (unsigned)A.pool.page_blocks;
-      const long long off = page_ok ? ((long long)U.id * Hkv + g) * A.pool.head_bytes + (long long)in * kBlk : 0;
-      const uint32_t dst = ring_a + issued * kBlk;
-      if (!U.list) {
-        if (m && lane == 0) {
-          if (was_list >> issued & 1u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          bulk_load(dst, A.pool.pages + off, kBlk, bar_a + 8 * issued, pol);
+  // Every unit arrives once at its slot's barrier: with its copy, or plainly.
+  auto issue = [&]() {
+    if (ki < nk) {
+      const uint32_t dst = ring_a + islot * U * kBlk, bar = bar_a + 8 * islot;
+      const bool mine = lane / U == ki % kItems;
+      const bool gather = LISTED && mine && (cur.info & kList);
+      if (mine && !gather) {
+        vmask[(warp * S + islot) * U + lane % U] = cur.info;
+        if (cur.info) {
+          if (LISTED && (was_list >> islot & 1u)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          bulk_load(dst + lane % U * kBlk, A.pool.pages + cur.off, kBlk, bar, pol);
+        } else {
+          mbar_arrive(bar, 1);
         }
-        was_list &= ~(1u << issued);
-      } else {
-        was_list |= 1u << issued;
-        const long long at = off + (U.pos & (kBlockTok - 1));   // block offset (a multiple of 256) and row
+      }
+      if (LISTED) was_list &= ~(1u << islot);
+      if (LISTED && __any_sync(kFull, gather)) {
+        was_list |= 1u << islot;
+        const bool page_ok = (unsigned)r0.id < (unsigned)A.pool.n_pages;
+        if (r0.pos >= 0 && !page_ok) atomicOr(A.pool.err, kErrPage);
+        const unsigned m = __ballot_sync(kFull, r0.pos >= 0 && page_ok);
+        const unsigned in = ((unsigned)r0.pos / kBlockTok) % (unsigned)A.pool.page_blocks;
+        // block offset (a multiple of 256) and row
+        const long long from = page_ok ? ((long long)r0.id * Hkv + r0.s % Hkv) * A.pool.head_bytes + (long long)in * kBlk +
+                                             (r0.pos & (kBlockTok - 1)) : 0;
         if (FMT == kPageInt4) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = i * 8 + gid;
-            const long long a = __shfl_sync(kFull, at, r);
+          for (int i = 0; i < 2 * U; ++i) {
+            const int r = i * 8 + gid;   // row of the item
+            const long long a = __shfl_sync(kFull, from, r);
             if (m >> r & 1u) {
               const int rin = (int)(a & 15);
               const unsigned char* src = A.pool.pages + (a - rin) + rin * kRow4 + t4 * 16;
-              cp_async16(dst + r * kRow4 + t4 * 16, src);
-              cp_async16(dst + kBlockTok * kRow4 + r * kRow4 + t4 * 16, src + kBlockTok * kRow4);
+              const uint32_t d = dst + i / 2 * kBlk + (r & 15) * kRow4 + t4 * 16;
+              cp_async16(d, src);
+              cp_async16(d + kBlockTok * kRow4, src + kBlockTok * kRow4);
             }
           }
-          if (lane < 16 && (m >> lane & 1u)) {
-            const int rin = (int)(at & 15);
-            cp_async16(dst + 2 * kBlockTok * kRow4 + lane * 16, A.pool.pages + (at - rin) + 2 * kBlockTok * kRow4 + rin * 16);
+          if (m >> lane & 1u) {
+            const int rin = (int)(from & 15);
+            cp_async16(dst + lane / 16 * kBlk + 2 * kBlockTok * kRow4 + (lane & 15) * 16,
+                       A.pool.pages + (from - rin) + 2 * kBlockTok * kRow4 + rin * 16);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = i * 2 + (lane >> 4), c = lane & 15;
-            const long long a = __shfl_sync(kFull, at, r);
+            const long long a = __shfl_sync(kFull, from, r);
             if (m >> r & 1u) {
               const int rin = (int)(a & 15);
               const unsigned char* src = A.pool.pages + (a - rin) + rin * 256 + ((c ^ (rin & 7)) << 4);
@@ -337,134 +451,212 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
             }
           }
         }
+        if (gather) {
+          vmask[(warp * S + islot) * U + lane % U] = (m >> lane % U * 16 & 0xffffu) | kList;
+          mbar_arrive(bar, 1);
+        }
       }
-      if (lane == 0) vmask[warp * S + issued] = m | (U.list ? 0x10000u : 0u);
-      issued = issued + 1 == S ? 0 : issued + 1;
+      islot = islot + 1 == S ? 0 : islot + 1;
     }
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
-  };
-  Unit ub = next_unit();
-  load_page(ub);
-  Unit ua = next_unit();
-  auto step = [&]() {
-    issue(ub);
-    ub = ua;
-    load_page(ub);
-    ua = next_unit();
+    if (LISTED) asm volatile("cp.async.commit_group;\n" ::: "memory");
+    ++ki;
+    if (LISTED) {   // the items behind: found two early, for the lists' pipeline
+      if ((ki + 2) % kItems == 0) nxt = find(ki + 2);
+      if (ki % kItems == 0) cur = nxt;
+      r0 = r1;
+      list_pages(r0);
+      r1 = list_rows(ki + 1);
+    } else if (ki % kItems == 0) {
+      cur = find(ki);
+    }
   };
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i) step();
+  for (int i = 0; i < S - 1; ++i) issue();
 
-  int slot = 0;           // ring slot to consume
-  unsigned parity = 0u;   // phase of each slot's barrier
+  const uint32_t qf_a = smem_u32(qf) + lane * 16;
+  int slot = 0;         // ring slot to consume
+  unsigned phase = 0u;  // of its barrier
+  int i = warp;         // its item, from r_lo
 
   for (int s = s_first; s <= s_last; ++s) {
-    int u0, n_u;
-    piece(s, u0, n_u);
-    if (n_u == 0) continue;
+    if (rpre[s + 1] == rpre[s]) continue;
+    const int i_end = (int)(min(r_hi, rpre[s + 1]) - r_lo);
     const int b = s / Hkv, g = s - b * Hkv;
     const size_t h0 = (size_t)b * A.Hq + (size_t)g * G;
     // ---- the group's queries, rotated at position L - 1, times scale / ln 2
     {
       const int pos = sinfo[s].x - 1, half = tab.rot / 2;
-      for (int i = tid; i < G * (kHeadDim / 2); i += kWarps * 32) {
-        const int h = i >> 6, j = i & 63;
+      for (int x = tid; x < G * (kHeadDim / 2); x += W * 32) {
+        const int h = x >> 6, j = x & 63;
         const int d0 = j >= half ? tab.rot + 2 * (j - half) : tab.interleaved ? 2 * j : j;
         const int d1 = j >= half || tab.interleaved ? d0 + 1 : d0 + half;
-        float x, y;
+        float q0, q1;
         if (A.q_f32) {
           const float* q = static_cast<const float*>(A.q) + (h0 + h) * kHeadDim;
-          x = q[d0];
-          y = q[d1];
+          q0 = q[d0];
+          q1 = q[d1];
         } else {
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + (h0 + h) * kHeadDim;
-          x = __bfloat162float(q[d0]);
-          y = __bfloat162float(q[d1]);
+          q0 = __bfloat162float(q[d0]);
+          q1 = __bfloat162float(q[d1]);
         }
         float c = 1.f, sn = 0.f;
         if (j < half) rope_cs(tab.f_pi[j], (double)pos, (float)tab.mag, c, sn);
-        qs[h * kHeadDim + d0] = (x * c - y * sn) * A.scale_log2;
-        qs[h * kHeadDim + d1] = (x * sn + y * c) * A.scale_log2;
+        qs[h * kHeadDim + d0] = (q0 * c - q1 * sn) * A.scale_log2;
+        qs[h * kHeadDim + d1] = (q0 * sn + q1 * c) * A.scale_log2;
       }
       __syncthreads();
     }
-    // A operand: 4 bits: k-step 2w + i of word w holds dims 32 t4 + 8 w + 2 i + {0, 4, 1, 5}; bf16: natural order
-    uint32_t qa[8][4];
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const float* q = qs + (gid < G ? gid : 0) * kHeadDim;
-      float x[4];
-      if (FMT == kPageInt4) {
-        const int d = 32 * t4 + 8 * (kk >> 1) + 2 * (kk & 1);
-        x[0] = q[d];
-        x[1] = q[d + 4];
-        x[2] = q[d + 1];
-        x[3] = q[d + 5];
-      } else {
-        const int d = 16 * kk + 2 * t4;
-        x[0] = q[d];
-        x[1] = q[d + 1];
-        x[2] = q[d + 8];
-        x[3] = q[d + 9];
+    // A operand: 4 bits: k-step 2w + i of word w holds dims 32 t4 + 8 w + 2 i + {0, 4, 1, 5}, in shared
+    // memory; bf16: natural order, in registers
+    uint32_t qa[kF16 ? 1 : 8][4];
+    uint32_t qb[WIDE ? 8 : 1][2];   // the low part's rows where they need a product of their own
+    float unscale = 1.f;
+    if (kF16) {
+      const float* q = qs + (gid < G ? gid : 0) * kHeadDim + 32 * t4;
+      float top = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(q[i]));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
+      const float f = gid < G ? __uint_as_float((unsigned)(127 + 10 - e) << 23) : 0.f;
+      unscale = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kCodeUnit;
+      for (int kk = warp; kk < 8; kk += W) {
+        const float* x = q + 8 * (kk >> 1) + 2 * (kk & 1);
+        __half2 h[2], lo[2];
+        split_f16(x[0] * f, x[4] * f, h[0], lo[0]);
+        split_f16(x[1] * (f * 0.0625f), x[5] * (f * 0.0625f), h[1], lo[1]);
+        qf[32 * kk + lane] = make_uint4(bits(h[0]), bits(lo[0]), bits(h[1]), bits(lo[1]));
       }
-      if (gid >= G) x[0] = x[1] = x[2] = x[3] = 0.f;
-      split2(x[0], x[1], qa[kk][0], qa[kk][1]);
-      split2(x[2], x[3], qa[kk][2], qa[kk][3]);
+      __syncthreads();
+      if (warp < 4) {
+        float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const uint4 v = qf[32 * (2 * warp + kk) + lane];
+          const float2 h0_ = __half22float2(half2_of(v.x)), l0 = __half22float2(half2_of(v.y));
+          const float2 h1 = __half22float2(half2_of(v.z)), l1 = __half22float2(half2_of(v.w));
+          t.x += (h0_.x + h0_.y) + 16.f * (h1.x + h1.y);
+          t.y += (l0.x + l0.y) + 16.f * (l1.x + l1.y);
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          t.x += __shfl_xor_sync(kFull, t.x, o);
+          t.y += __shfl_xor_sync(kFull, t.y, o);
+        }
+        if (t4 == 0) q8[8 * warp + gid] = make_float2(t.x * (-8.f / kCodeUnit), t.y * (-8.f / kCodeUnit));
+      }
+      __syncthreads();
+    } else {
+      const int h = WIDE ? gid : gid & 3;
+      const bool in = h < G;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const float* x = qs + (in ? h : 0) * kHeadDim + 16 * kk + 2 * t4;
+        uint32_t hi[2], mid[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_bf16(in ? x[8 * i] : 0.f, in ? x[8 * i + 1] : 0.f, hi[i], mid[i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qa[kF16 ? 0 : kk][2 * i] = WIDE || gid < 4 ? hi[i] : mid[i];
+          qa[kF16 ? 0 : kk][2 * i + 1] = WIDE ? mid[i] : gid < 4 ? lo[i] : 0u;
+          if (WIDE) qb[WIDE ? kk : 0][i] = lo[i];
+        }
+      }
     }
     float m = kNoMax, l = 0.f;
+    unsigned vlim = kScaleLow;                                        // 4 bits: bound of the value scales met (bf16 bits)
+    float vmul = kScaleTop * __uint_as_float((254u << 23) - (kScaleLow << 16));   // kScaleTop / bound
     float acc[16][4];
 #pragma unroll
     for (int nt = 0; nt < 16; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 
 #pragma unroll 1
-    for (int u = warp; u < n_u; u += kWarps) {
+    for (; i < i_end; i += W) {
       __syncwarp();
-      step();   // refills the slot consumed last time
-      const unsigned vm = vmask[warp * S + slot];
-      const unsigned char* st = myring + slot * kBlk;
-      const int my_slot = slot;
-      slot = slot + 1 == S ? 0 : slot + 1;
-      const unsigned rows = vm & 0xffffu;
-      if (vm & 0x10000u) {
+      issue();   // refills the slot consumed last time
+      const unsigned char* const st = ring + (warp * S + slot) * U * kBlk;
+      if (!mbar_wait(bar_a + 8 * slot, phase) && lane == 0) atomicOr(A.pool.err, kErrTimeout);
+      unsigned vm[U], any = 0u, all = 0xffffu;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        vm[u] = vmask[(warp * S + slot) * U + u];
+        any |= vm[u];
+        all &= vm[u];
+      }
+      if (++slot == S) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (LISTED && (any & kList)) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 1) : "memory");
         __syncwarp();
-      } else if (rows) {
-        if (!mbar_wait(bar_a + 8 * my_slot, parity >> my_slot & 1u)) {
-          if (lane == 0) atomicOr(A.pool.err, kErrTimeout);
-        }
-        parity ^= 1u << my_slot;
       }
-      if (!rows) continue;
-
-      // ---- scores of head gid for rows 8 j + 2 t4 + e
-      float sc[2][2];
-      uint4 rs[2][2];   // 4 bits: the rows' scales
-      if (FMT == kPageInt4) {
-        uint4 kw[2];
+      if (!(any & 0xffffu)) continue;
+      const bool part = (all & 0xffffu) != 0xffffu;
+      // ---- 4 bits: lane l widens the scales of row l of the item, those of V times vmul to float16
+      if (kF16) {
+        uint4 w = *reinterpret_cast<const uint4*>(st + lane / 16 * kBlk + 2 * kBlockTok * kRow4 + (lane & 15) * 16);
+        if (part && !((lane < 16 ? vm[0] : vm[U - 1]) >> (lane & 15) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t vtop = max_u16x2(w.z, w.w);
+        vtop = max(vtop & 0xffffu, vtop >> 16);
+        if (__any_sync(kFull, vtop > vlim)) {
+          if (vtop >= 0x7f80u) {   // a NaN scale: the finite ones decide
+            auto finite = [](uint32_t x) { return x < 0x7f80u ? x : 0u; };
+            vtop = max(max(finite(w.z & 0xffffu), finite(w.z >> 16)), max(finite(w.w & 0xffffu), finite(w.w >> 16)));
+          }
+          vtop = __reduce_max_sync(kFull, vtop);
+          if (vtop > vlim) {   // the power of two at or above it (2^126 at most: its reciprocal is a normal number)
+            vlim = min((vtop + 0x7fu) & 0x7f80u, 0x7e80u);
+            const float now = kScaleTop * __uint_as_float((254u << 23) - (vlim << 16)), by = now / vmul;
+            vmul = now;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          kw[j] = *reinterpret_cast<const uint4*>(st + (8 * j + gid) * kRow4 + t4 * 16);
+            for (int nt = 0; nt < 16; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            rs[j][e] = *reinterpret_cast<const uint4*>(st + 2 * kBlockTok * kRow4 + (8 * j + 2 * t4 + e) * 16);
+              for (int i = 0; i < 4; ++i) acc[nt][i] *= by;
+          }
         }
+        kscale[128 * warp + lane] = bf16_lo(w.x);
+        kscale[128 * warp + 32 + lane] = bf16_hi(w.x);
+        kscale[128 * warp + 64 + lane] = bf16_lo(w.y);
+        kscale[128 * warp + 96 + lane] = bf16_hi(w.y);
+        const uint32_t a01 = bits(__floats2half2_rn(bf16_lo(w.z) * vmul, bf16_hi(w.z) * vmul));
+        const uint32_t a23 = bits(__floats2half2_rn(bf16_lo(w.w) * vmul, bf16_hi(w.w) * vmul));
+        const uint32_t b01 = __shfl_down_sync(kFull, a01, 1), b23 = __shfl_down_sync(kFull, a23, 1);
+        if (!(lane & 1))
+          vscale[16 * warp + lane / 2] = make_uint4(__byte_perm(a01, b01, 0x5410), __byte_perm(a01, b01, 0x7632),
+                                                    __byte_perm(a23, b23, 0x5410), __byte_perm(a23, b23, 0x7632));
+        __syncwarp();
+      }
+      // ---- scores of head gid for rows 8 j + 2 t4 + e of unit u (4 bits: still to be multiplied by unscale)
+      float p[U][2][2];
+      if (kF16) {
+        uint4 kw[U][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w[4] = {kw[j].x, kw[j].y, kw[j].z, kw[j].w};
-          float d[4][4];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            d[g4][0] = d[g4][1] = d[g4][2] = d[g4][3] = 0.f;
-            mma16816(d[g4], qa[2 * g4], code_pair(w[g4], 0), code_pair(w[g4], 1));
-            mma16816(d[g4], qa[2 * g4 + 1], code_pair(w[g4], 2), code_pair(w[g4], 3));
-          }
+          for (int j = 0; j < 2; ++j)
+            kw[u][j] = *reinterpret_cast<const uint4*>(st + u * kBlk + (8 * j + gid) * kRow4 + t4 * 16);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a0 = bf16_lo(rs[j][e].x) * (d[0][e] + d[0][2 + e]);
-            const float a1 = bf16_hi(rs[j][e].x) * (d[1][e] + d[1][2 + e]);
-            sc[j][e] = fmaf(bf16_lo(rs[j][e].y), d[2][e] + d[2][2 + e], a0) +
-                       fmaf(bf16_hi(rs[j][e].y), d[3][e] + d[3][2 + e], a1);
-          }
+        for (int g4 = 0; g4 < 4; ++g4) {
+          const uint4 a0 = lds128(qf_a + 1024 * g4), a1 = lds128(qf_a + 1024 * g4 + 512);
+          const uint32_t a1r[4] = {a1.x, a1.y, a1.z, a1.w};
+          const float2 centre = q8[8 * g4 + gid];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = g4 == 0 ? kw[u][j].x : g4 == 1 ? kw[u][j].y : g4 == 2 ? kw[u][j].z : kw[u][j].w;
+              uint32_t c[4];
+              float d[4];
+              code_pairs(w, c);
+              mma16816_from(d, a0, c[0], c[1], centre);
+              mma16816<true>(d, a1r, c[2], c[3]);
+              const float2 k = *reinterpret_cast<const float2*>(kscale + 128 * warp + 32 * g4 + 16 * u + 8 * j + 2 * t4);
+              p[u][j][0] = g4 == 0 ? k.x * (d[0] + d[2]) : fmaf(k.x, d[0] + d[2], p[u][j][0]);
+              p[u][j][1] = g4 == 0 ? k.y * (d[1] + d[3]) : fmaf(k.y, d[1] + d[3], p[u][j][1]);
+            }
         }
       } else {
         float d[2][2][4];
@@ -478,91 +670,117 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
         for (int kk = 0; kk < 8; ++kk) {
           uint32_t bk[4];
           ldsm_x4(bk, row + (((2 * kk + (mi & 1)) ^ rr) << 4));
-          mma16816(d[0][kk & 1], qa[kk], bk[0], bk[1]);
-          mma16816(d[1][kk & 1], qa[kk], bk[2], bk[3]);
+          mma16816<false>(d[0][kk & 1], qa[kF16 ? 0 : kk], bk[0], bk[1]);
+          mma16816<false>(d[1][kk & 1], qa[kF16 ? 0 : kk], bk[2], bk[3]);
+          if (WIDE) {
+            const uint32_t low[4] = {qb[WIDE ? kk : 0][0], 0u, qb[WIDE ? kk : 0][1], 0u};
+            mma16816<false>(d[0][kk & 1], low, bk[0], bk[1]);
+            mma16816<false>(d[1][kk & 1], low, bk[2], bk[3]);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) sc[j][e] = (d[j][0][e] + d[j][1][e]) + (d[j][0][2 + e] + d[j][1][2 + e]);
+          for (int e = 0; e < 2; ++e) {
+            p[0][j][e] = (d[j][0][e] + d[j][1][e]) + (d[j][0][2 + e] + d[j][1][2 + e]);
+            if (!WIDE) p[0][j][e] += __shfl_xor_sync(kFull, p[0][j][e], 16);
+          }
       }
-      const bool part = rows != 0xffffu;
       if (part) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (!(rows >> (8 * j + 2 * t4 + e) & 1u)) {
-              sc[j][e] = -INFINITY;
-              rs[j][e].z = rs[j][e].w = 0u;
-            }
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(vm[u] >> (8 * j + 2 * t4 + e) & 1u)) p[u][j][e] = -INFINITY;
       }
-      // ---- running maximum and sum
-      float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      // ---- running maximum and sum; scores become probabilities
+      float mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mx = fmaxf(mx, fmaxf(p[u][j][0], p[u][j][1]));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const float mn = fmaxf(m, mx);
+      const float mn = fmaxf(m, fmaf(mx, unscale, kF16 ? -kProbExp : 0.f));
       if (__any_sync(kFull, mn != m)) {
         const float alpha = ex2(m - mn);
-#pragma unroll
-        for (int nt = 0; nt < 16; ++nt) {
-          acc[nt][0] *= alpha;
-          acc[nt][1] *= alpha;
-          acc[nt][2] *= alpha;
-          acc[nt][3] *= alpha;
-        }
         l *= alpha;
         m = mn;
+#pragma unroll
+        for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[nt][i] *= alpha;
       }
-      float p[2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[j][e] = ex2(sc[j][e] - mn);
-          l += p[j][e];
-        }
-      // ---- values
-      if (FMT == kPageInt4) {
-        const unsigned char* vb = st + kBlockTok * kRow4 + gid * 8;
-        uint2 vw[2][2];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) vw[j][e] = *reinterpret_cast<const uint2*>(vb + (8 * j + 2 * t4 + e) * kRow4);
+          for (int e = 0; e < 2; ++e) {
+            p[u][j][e] = ex2(fmaf(p[u][j][e], unscale, -m));
+            l += p[u][j][e];
+          }
+      // ---- acc += P V
+      if (kF16) {
 #pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4) {
-          float pv[2][2];
+        for (int u = 0; u < U; ++u) {
+          const unsigned char* vb = st + u * kBlk + kBlockTok * kRow4 + gid * 8;
+          uint2 vw[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t w = g4 < 2 ? rs[j][e].z : rs[j][e].w;
-              pv[j][e] = p[j][e] * ((g4 & 1) ? bf16_hi(w) : bf16_lo(w));
+            for (int e = 0; e < 2; ++e) vw[j][e] = *reinterpret_cast<const uint2*>(vb + (8 * j + 2 * t4 + e) * kRow4);
+          __half2 ph[2], pl[2];
+          uint32_t sv[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            split_f16(p[u][j][0], p[u][j][1], ph[j], pl[j]);
+            const uint4 v = vscale[16 * warp + 8 * u + 4 * j + t4];
+            sv[j][0] = v.x;
+            sv[j][1] = v.y;
+            sv[j][2] = v.z;
+            sv[j][3] = v.w;
+          }
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            uint32_t pa[4], w[2], c0[4], c1[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // high part of the product; its exact rounding error and the low part make the residual
+              const __half2 sg = half2_of(sv[j][g4]);
+              const __half2 hi = __hmul2(ph[j], sg);
+              pa[2 * j] = bits(hi);
+              pa[2 * j + 1] = bits(__hfma2(pl[j], sg, __hfma2(ph[j], sg, __hneg2(hi))));
+              w[j] = g4 < 2 ? __byte_perm(vw[j][0].x, vw[j][1].x, (g4 & 1) ? 0x7632 : 0x5410)
+                            : __byte_perm(vw[j][0].y, vw[j][1].y, (g4 & 1) ? 0x7632 : 0x5410);
             }
-          uint32_t pa[4];
-          split2(pv[0][0], pv[0][1], pa[0], pa[1]);
-          split2(pv[1][0], pv[1][1], pa[2], pa[3]);
-          uint32_t w[2];
+            centred_pairs(w[0], c0);
+            centred_pairs(w[1], c1);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[j] = g4 < 2 ? __byte_perm(vw[j][0].x, vw[j][1].x, (g4 & 1) ? 0x7632 : 0x5410)
-                          : __byte_perm(vw[j][0].y, vw[j][1].y, (g4 & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) mma16816(acc[4 * g4 + t], pa, code_pair(w[0], t), code_pair(w[1], t));
+            for (int t = 0; t < 4; ++t) mma16816<true>(acc[4 * g4 + t], pa, c0[t], c1[t]);
+          }
         }
       } else {
-        uint32_t pa[4];
-        split2(p[0][0], p[0][1], pa[0], pa[1]);
-        split2(p[1][0], p[1][1], pa[2], pa[3]);
+        uint32_t pa[4], pb[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t hi, mid, lo;
+          split_bf16(p[0][j][0], p[0][j][1], hi, mid, lo);
+          pa[2 * j] = WIDE || gid < 4 ? hi : mid;
+          pa[2 * j + 1] = WIDE ? mid : gid < 4 ? lo : 0u;
+          pb[2 * j] = lo;
+          pb[2 * j + 1] = 0u;
+        }
         const int mi = lane >> 3, rr = lane & 7;
         const uint32_t row = smem_u32(st) + kBlockTok * 256 + (8 * (mi & 1) + rr) * 256;
         // rows 2 t4 + {0, 1} and + 8 as bit masks of the operand's halves
         uint32_t live0 = kFull, live1 = kFull;
         if (part) {
-          const unsigned r0 = rows >> (2 * t4), r1 = rows >> (8 + 2 * t4);
-          live0 = ((r0 & 1u) ? 0xffffu : 0u) | ((r0 & 2u) ? 0xffff0000u : 0u);
-          live1 = ((r1 & 1u) ? 0xffffu : 0u) | ((r1 & 2u) ? 0xffff0000u : 0u);
+          const unsigned v0 = vm[0] >> (2 * t4), v1 = vm[0] >> (8 + 2 * t4);
+          live0 = ((v0 & 1u) ? 0xffffu : 0u) | ((v0 & 2u) ? 0xffff0000u : 0u);
+          live1 = ((v1 & 1u) ? 0xffffu : 0u) | ((v1 & 2u) ? 0xffff0000u : 0u);
         }
 #pragma unroll
         for (int nt = 0; nt < 16; nt += 2) {
@@ -574,8 +792,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
             bv[2] &= live0;
             bv[3] &= live1;
           }
-          mma16816(acc[nt], pa, bv[0], bv[1]);
-          mma16816(acc[nt + 1], pa, bv[2], bv[3]);
+          mma16816<false>(acc[nt], pa, bv[0], bv[1]);
+          mma16816<false>(acc[nt + 1], pa, bv[2], bv[3]);
+          if (WIDE) {
+            mma16816<false>(acc[nt], pb, bv[0], bv[1]);
+            mma16816<false>(acc[nt + 1], pb, bv[2], bv[3]);
+          }
         }
       }
     }
@@ -586,8 +808,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
     float o[16][2];
 #pragma unroll
     for (int nt = 0; nt < 16; ++nt) {
-      o[nt][0] = acc[nt][0] + acc[nt][2];
-      o[nt][1] = acc[nt][1] + acc[nt][3];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        o[nt][e] = acc[nt][e] + acc[nt][2 + e];
+        if (kF16) o[nt][e] *= ((nt & 1) ? kCodeUnit / 16.f : kCodeUnit) / vmul;
+        else if (!WIDE) o[nt][e] += __shfl_xor_sync(kFull, o[nt][e], 16);
+      }
     }
     // dims of (column tile nt, e): 4 bits 32 t4 + 16 e + nt, bf16 8 nt + 2 t4 + e
     auto put = [&](float* dst) {
@@ -612,8 +838,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
         }
     };
 #pragma unroll 1
-    for (int half = kWarps / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half && gid < G) {
+    for (int n = W; n > 1; n = (n + 1) / 2) {
+      const int half = (n + 1) / 2;   // warps half .. n - 1 hand over to 0 ..
+      if (warp >= half && warp < n && gid < G) {
         float* dst = mbuf + ((size_t)(warp - half) * kMaxGroup + gid) * kPartStride;
         put(dst);
         if (t4 == 0) {
@@ -622,7 +849,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
         }
       }
       __syncthreads();
-      if (warp < half && gid < G) {
+      if (warp < n - half && gid < G) {
         const float* src = mbuf + ((size_t)warp * kMaxGroup + gid) * kPartStride;
         const float m2 = src[kHeadDim], l2 = src[kHeadDim + 1];
         const float mn = fmaxf(m, m2);
@@ -662,13 +889,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
     __syncthreads();
     if (!s_merge) continue;
     __threadfence();
-    // warp w: head w % G, states c0 + w / G, c0 + w / G + per, ...; then the warps of a head in order
+    // part x of G per: head x % G, states c0 + x / G, c0 + x / G + per, ...; then the parts of a head in order
     {
-      const int per = max(1, kWarps / G);
-      const int h = warp % G, sub = warp / G;
-      float M = kNoMax, Ls = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sub < per) {
+      const int per = max(1, W / G);
+      for (int x = warp; x < G * per; x += W) {
+        const int h = x % G, sub = x / G;
+        float M = kNoMax, Ls = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kB = 8;
         for (int c = c0 + sub; c <= c1; c += per * kB) {
           float4 v[kB];
@@ -698,20 +925,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
             M = mn;
           }
         }
-      }
-      float* mine = cbuf + (size_t)warp * kPartStride;
-      *reinterpret_cast<float4*>(mine + 4 * lane) = num;
-      if (lane == 0) {
-        mine[kHeadDim] = M;
-        mine[kHeadDim + 1] = Ls;
+        float* mine = cbuf + (size_t)x * kPartStride;
+        *reinterpret_cast<float4*>(mine + 4 * lane) = num;
+        if (lane == 0) {
+          mine[kHeadDim] = M;
+          mine[kHeadDim + 1] = Ls;
+        }
       }
       __syncthreads();
-      if (warp < G) {
-        M = kNoMax;
-        Ls = 0.f;
-        num = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int h = warp; h < G; h += W) {
+        float M = kNoMax, Ls = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < per; ++k) {
-          const float* src = cbuf + (size_t)(warp + G * k) * kPartStride;
+          const float* src = cbuf + (size_t)(h + G * k) * kPartStride;
           const float m2 = src[kHeadDim], l2 = src[kHeadDim + 1];
           const float mn = fmaxf(M, m2);
           const float sa = exp2f(M - mn), sb = exp2f(m2 - mn);
@@ -724,50 +950,61 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attend_paged(const PagedAtte
           M = mn;
         }
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
-        reinterpret_cast<float4*>(A.out + (h0 + warp) * kHeadDim)[lane] = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-        if (A.lse && lane == 0) A.lse[h0 + warp] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
+        reinterpret_cast<float4*>(A.out + (h0 + h) * kHeadDim)[lane] = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        if (A.lse && lane == 0) A.lse[h0 + h] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
       }
       if (tid == 0) A.ticket[s] = 0u;   // ready for the next call
       __syncthreads();
     }
   }
-  asm volatile("cp.async.wait_all;\n" ::: "memory");
 }
 
-size_t smem_bytes(int format, int stages, int n_slices) {
-  const size_t blk = format == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
-  return kWarps * stages * blk + (size_t)(4 * kMaxGroup + kWarps) * kPartStride * 4 + kMaxGroup * kHeadDim * 4 +
+template <int FMT, int W, int U, int S>
+constexpr size_t smem_bytes(int n_slices) {
+  const size_t blk = FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
+  return W * U * S * blk + (size_t)((W + 1) / 2 * kMaxGroup + (W > kMaxGroup ? W : kMaxGroup)) * kPartStride * 4 + kMaxGroup * kHeadDim * 4 +
          (size_t)(n_slices + 1) * 8 + (size_t)n_slices * 8;
 }
-constexpr size_t kSmemMost = 226 * 1024;   // of 227 KB, less the static arrays
-constexpr int kStages4 = 6, kStages16 = 3, kStages16Many = 2;
-// bf16 blocks: three ring slots a warp where the slices' prefix leaves room for them, else two.
-int stages_for(int format, int n_slices) {
-  if (format == kPageInt4) return kStages4;
-  return smem_bytes(format, kStages16, n_slices) <= kSmemMost ? kStages16 : kStages16Many;
-}
+constexpr size_t smem_most(int format) { return (format == kPageInt4 ? 212 : 226) * 1024; }   // 227 KB less the static arrays
+// Warps, units an item, ring slots; the deeper ring where the slices' prefix leaves room for it.
+constexpr int kW4 = 12, kU4 = 2, kS4 = 3, kS4Many = 2;
+constexpr int kW16 = 8, kU16 = 1, kS16 = 3, kS16Many = 2;
 
-template <int FMT, int S>
-int setup_one() {
-  return cudaFuncSetAttribute(k_attend_paged<FMT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost) == cudaSuccess;
+template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
+bool setup_one() {
+  return cudaFuncSetAttribute(k_attend_paged<FMT, W, U, S, WIDE, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)smem_most(FMT)) == cudaSuccess;
 }
-template <int FMT, int S>
+template <int FMT, int W, int U, int S, int SMANY, bool WIDE>
+bool setup() {
+  static_assert(smem_bytes<FMT, W, U, SMANY>(kMaxPagedSlices) <= smem_most(FMT), "the shallow ring fits every call");
+  return setup_one<FMT, W, U, S, WIDE, false>() && setup_one<FMT, W, U, S, WIDE, true>() &&
+         setup_one<FMT, W, U, SMANY, WIDE, false>() && setup_one<FMT, W, U, SMANY, WIDE, true>();
+}
+template <int FMT, int W, int U, int S, bool WIDE>
+void launch(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
+  const size_t n = smem_bytes<FMT, W, U, S>(a.n_slices);
+  if (a.list) k_attend_paged<FMT, W, U, S, WIDE, true><<<grid, W * 32, n, st>>>(a, tab);
+  else k_attend_paged<FMT, W, U, S, WIDE, false><<<grid, W * 32, n, st>>>(a, tab);
+}
+template <int FMT, int W, int U, int S, int SMANY, bool WIDE>
 cudaError_t go(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
-  k_attend_paged<FMT, S><<<grid, kWarps * 32, smem_bytes(FMT, S, a.n_slices), st>>>(a, tab);
+  if (smem_bytes<FMT, W, U, S>(a.n_slices) <= smem_most(FMT)) launch<FMT, W, U, S, WIDE>(a, grid, tab, st);
+  else launch<FMT, W, U, SMANY, WIDE>(a, grid, tab, st);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int page_attend_setup(int format) {
-  if (format == kPageInt4) return setup_one<kPageInt4, kStages4>();
-  return setup_one<kPageBf16, kStages16>() && setup_one<kPageBf16, kStages16Many>();
+  if (format == kPageInt4) return setup<kPageInt4, kW4, kU4, kS4, kS4Many, false>();
+  return setup<kPageBf16, kW16, kU16, kS16, kS16Many, false>() && setup<kPageBf16, kW16, kU16, kS16, kS16Many, true>();
 }
 
 cudaError_t launch_page_attend(const PagedAttendArgs& a, int format, int grid, const RopeTab128& tab, cudaStream_t st) {
-  if (format == kPageInt4) return go<kPageInt4, kStages4>(a, grid, tab, st);
-  return stages_for(format, a.n_slices) == kStages16 ? go<kPageBf16, kStages16>(a, grid, tab, st)
-                                                      : go<kPageBf16, kStages16Many>(a, grid, tab, st);
+  if (format == kPageInt4) return go<kPageInt4, kW4, kU4, kS4, kS4Many, false>(a, grid, tab, st);
+  return a.G <= 4 ? go<kPageBf16, kW16, kU16, kS16, kS16Many, false>(a, grid, tab, st)
+                  : go<kPageBf16, kW16, kU16, kS16, kS16Many, true>(a, grid, tab, st);
 }
 
 }  // namespace spa
