@@ -12,32 +12,69 @@
 //
 // Rounding to 4 bits: scale = bf16(amax / 7), code = clamp(round_even(x / scale), -7, 7) + 8.
 // Sixteen levels lose one to the symmetric range, and need no offset beside the scale: 144 bytes a
-// row pair instead of 160.  Every decision is the one exact arithmetic takes: a float32
-// quotient within its error of a border is decided again by an exact product (rows that are
-// stored as given), or the whole row is computed again in 64 bits (rotated keys; about 1 row in 500).
+// row pair instead of 160.  Every decision is the one exact arithmetic takes.  bf16 rows stored as
+// given have 8 bits, so their scales and quotients are far from a border or exactly on it, and float32 decides both;
+// a rotated key within the rotation's error of a border (1 row in 300), a float32 row near one and a group
+// that is tiny or not finite take a second, exact way: products of few bits, and 64 bits for the rotation.
 //
-// Bound by memory: a row pair moves 512 + 144 bytes at bf16.  16 lanes own the K and V rows of one
-// (token, head), 8 dims each: 16-byte loads, one 32-bit code word a lane, group maxima in 2-3 shuffles.
-// A lane's cosines and sines serve all the heads it takes of its token.
+// Bound by memory: a row pair moves 512 + 144 bytes at bf16.  8 lanes own the K and V rows of one (token, head),
+// lane e the dims 8 e .. 8 e + 7 and 64 further of both: the pairs of a whole-head rotation meet in one lane, its 16
+// dims are of one scale group of K and of two of V (group maxima in 1 and 2 shuffles), and every
+// load and code word is 16 and 4 bytes.  A lane's cosines and sines serve all the heads it takes of its token.
 #include "spa_paged.cuh"
 
 namespace spa {
 namespace {
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(u[i]);
-    f[2 * i + 1] = bf16_hi(u[i]);
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 8 dims of a row as loaded.  top(): float bits of the largest magnitude, NaN above infinity.
+template <typename T>
+struct Dims;
+template <>
+struct Dims<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  // largest magnitudes of the even and the odd dims of words i and i + 1, 16 bits each
+  __device__ __forceinline__ uint32_t top2(int i) const { return max_u16x2(w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu); }
+  __device__ __forceinline__ unsigned top() const {
+    const uint32_t m = max_u16x2(top2(0), top2(2));
+    return max(m << 16, m & 0xffff0000u);
+  }
+};
+template <>
+struct Dims<float> {
+  float f[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void get(float (&g)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = f[i];
+  }
+  __device__ __forceinline__ unsigned top4(int i) const {
+    unsigned m = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[i + j]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ unsigned top() const { return max(top4(0), top4(4)); }
+};
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t u[4];
 #pragma unroll
@@ -53,40 +90,56 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// bf16(x / 7) rounded to nearest even, x >= 0 finite.  The bf16 below is found by division; the
-// border above it has 9 significant bits, so 7 times it is exact in float32 and decides.
+constexpr float kSeventh = 0.142857149f;
+// Groups this small (2^-110: the reciprocal of their scale would overflow) are stored as zeros.
+constexpr unsigned kTinyBits = 0x08800000u;
+constexpr unsigned kInfBits = 0x7f800000u;
+__device__ __forceinline__ bool odd_group(unsigned top) { return top - kTinyBits >= kInfBits - kTinyBits; }
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float bf16_of(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+// Rounding by the sum with 1.5 * 2^23 + 8: the float's bits are kMagicBits + n + 8.  |x / s| stays below 7.04 (the
+// scale is off by 2^-8 at most), so n needs no clamp.
+constexpr float kMagic = 12582920.f;
+constexpr unsigned kMagicBits = 0x4b400000u;
+// Word of 8 codes out of such bits: their sum times 16^i, less the constants' (modulo 2^32).
+__device__ __forceinline__ unsigned pack_codes(const float (&t)[8]) {
+  unsigned w = __float_as_uint(t[7]);
+#pragma unroll
+  for (int i = 6; i >= 0; --i) w = w * 16u + __float_as_uint(t[i]);
+  return w - kMagicBits * 0x11111111u;
+}
+// The codes of 4 bf16 values under s: the quotient with one correction is exact where it is a tie (8 bits by 8
+// bits: other quotients are 2^-17 away from one), so the sum rounds as the definition does.
+__device__ __forceinline__ void round4(const float* x, float s, float inv, float* t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q = x[i] * inv;
+    t[i] = fmaf(fmaf(-q, s, x[i]), inv, q) + kMagic;
+  }
+}
+
+// ---- the exact way
+// Scale of a group with largest magnitude x (float or double, >= 0; NaN above infinity): bf16(x / 7), ties to even.  The
+// bf16 at or next below is found by a product; the border above that has 9 significant bits, so 7
+// times it is exact and decides.
 template <typename F>
-__device__ __forceinline__ float seventh(F x) {
-  const unsigned u = __float_as_uint((float)x / 7.f) & 0xffff0000u;
-  const float border = __uint_as_float(u | 0x8000u);
-  const F b7 = (F)border * (F)7;
-  const bool up = x > b7 || (x == b7 && (u & 0x10000u));
+__device__ float exact_scale(F x) {
+  if (!(x <= (F)3.4028235e38f)) return __uint_as_float(0x7fc00000u);
+  if (x < (F)__uint_as_float(kTinyBits)) return 0.f;
+  const unsigned u = __float_as_uint((float)x * kSeventh) & 0xffff0000u;
+  const F border7 = (F)__uint_as_float(u | 0x8000u) * (F)7;
+  const bool up = x > border7 || (x == border7 && (u & 0x10000u));
   return __uint_as_float(up ? u + 0x10000u : u);
 }
-// Groups this small (2^-110: the reciprocal of their scale would overflow) are stored as zeros.
-constexpr float kTiny = 7.7037198e-34f;
-__device__ __forceinline__ float group_scale(float amax) {
-  if (!(amax <= 3.4028235e38f)) return __uint_as_float(0x7fc00000u);   // infinity or NaN in the group
-  return amax < kTiny ? 0.f : seventh(amax);
-}
-
-// Code 1..15 of x under scale s (inv = 1 / s), decided exactly.
-__device__ __forceinline__ unsigned code_exact(float x, float s, float inv) {
-  const float q = x * inv;
-  float n = rintf(q);
-  if (fabsf(fabsf(q - n) - 0.5f) < 1e-5f) {
-    const float k = floorf(fabsf(q)), border = (k + 0.5f) * s;   // 4 bits times 8 bits: exact
-    const float ax = fabsf(x);
-    const float m = ax > border ? k + 1.f : ax < border ? k : 2.f * rintf(0.5f * (k + 0.5f));   // a tie goes to the even one
-    n = copysignf(m, x);
-  }
-  return (unsigned)((int)fminf(fmaxf(n, -7.f), 7.f) + 8);
-}
-
 template <typename F>
 __device__ __forceinline__ F shfl_max(unsigned mask, F v, int o) {
   const F w = __shfl_xor_sync(mask, v, o);
-  return w > v ? w : v;
+  return max(w, v);
 }
 
 // Page base of (sequence b, position pos, head 0), or null.
@@ -118,174 +171,347 @@ __device__ __forceinline__ int row_count(const int64_t* n, int b, int T, unsigne
   return (int)v;
 }
 
-// PAIR: how a lane gets the partners of its 8 dims.
+// PAIR: where the partner of a dim is.
 constexpr int kNone = 0;      // no rotation
-constexpr int kInLane = 1;    // interleaved pairs
-constexpr int kShuffle = 2;   // halves, rot / 2 a multiple of 8: the partners are one lane's 8 dims
-constexpr int kReload = 3;    // halves, any rot: single loads
+constexpr int kInLane = 1;    // interleaved pairs: beside it
+constexpr int kWhole = 2;     // halves of the whole head: in the lane's other 8 dims
+constexpr int kFetch = 3;     // halves of a part of the head: loaded again
 
-template <typename T, int FMT, int PAIR>
-__global__ void __launch_bounds__(256) k_page_append(const PagePool P, const AppendArgs a, const __grid_constant__ RopeTab128 tab) {
-  const int lane = threadIdx.x & 31, e = lane & 15;
-  const unsigned mask = 0xffffu << (lane & 16);
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int64_t tok = item / a.head_groups;
-  if (tok >= (int64_t)a.B * a.T) return;
-  const int hg = (int)(item - tok * a.head_groups);
-  const int b = (int)(tok / a.T), t = (int)(tok - (int64_t)b * a.T);
-  if (t >= row_count(a.n_new, b, a.T, P.err)) return;
-  const int64_t pos = a.start[b] + t;
-  int blk, r;
-  unsigned char* const page = page_of(P, b, pos, blk, r);
-  if (!page) return;
-  const int half = tab.rot / 2;
-  const bool turned = PAIR != kNone && 8 * e < tab.rot;
+struct RowPair {
+  const void* k;        // the head's key row and value row
+  const void* v;
+  unsigned char* block;
+  int r;                // row in the block
+  int e;                // the lane's place, 0..7
+  unsigned mask;        // the row's lanes
+  double pos;
+};
 
-  // element i of the lane (dim 8 e + i) becomes x c[i] + partner sn[i]
-  float c[8], sn[8];
-  const float mag = (float)tab.mag;
-  if (PAIR == kInLane) {
+__device__ __forceinline__ void store_scales(const RowPair& R, float ks, float vs0, float vs1) {
+  // K group g in lane g; V groups 0, 1 in lane 0 and 2, 3 in lane 1
+  unsigned char* const sc = R.block + 2 * kBlockTok * kRow4 + R.r * 16;
+  if (R.e < 4) reinterpret_cast<unsigned short*>(sc)[R.e] = (unsigned short)(__float_as_uint(ks) >> 16);
+  if (R.e < 2) reinterpret_cast<unsigned*>(sc + 8)[R.e] = (__float_as_uint(vs0) >> 16) | (__float_as_uint(vs1) & 0xffff0000u);
+}
+
+// Codes of 8 values under s: the quotient in 64 bits, corrected once, is an exact tie where there is one and far enough
+// from one elsewhere (24 bits by 8), or known to 64 bits (rotated values).  8 everywhere where s is 0 or NaN.
+__device__ __forceinline__ unsigned exact_codes(const double* z, float s0, float s1) {
+  unsigned w = 0u;
+  const double i0 = 1.0 / (double)s0, i1 = 1.0 / (double)s1;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      c[i] = c[i + 1] = 1.f;
-      sn[i] = sn[i + 1] = 0.f;
-      if (8 * e + i < tab.rot) {
-        rope_cs(tab.f_pi[4 * e + i / 2], (double)pos, mag, c[i], sn[i + 1]);
-        c[i + 1] = c[i];
-        sn[i] = -sn[i + 1];
-      }
-    }
-  } else if (PAIR != kNone) {
+  for (int i = 0; i < 8; ++i) {
+    const double s = (double)(i < 4 ? s0 : s1), inv = i < 4 ? i0 : i1, q = z[i] * inv;
+    const int n = s > 0.0 ? (int)rint(fma(fma(-q, s, z[i]), inv, q)) : 0;
+    w |= (unsigned)(n + 8) << (4 * i);
+  }
+  return w;
+}
+// Rounds and stores a row pair by exact decisions.  Rarely called, and out of line: its registers are not the others'.
+template <typename T, int PAIR>
+__device__ __noinline__ void store_exact(const RowPair R, const RopeTab128& tab) {
+  const T* k = static_cast<const T*>(R.k) + 8 * R.e;
+  const T* v = static_cast<const T*>(R.v) + 8 * R.e;
+  const int half = tab.rot / 2;
+  const double inf = __longlong_as_double(0x7ff0000000000000ll);
+  double z[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = (double)Elem<T>::get(k, (i & 7) + 64 * (i >> 3));
+  if (PAIR == kWhole || PAIR == kInLane) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int d = 8 * e + i;
+      const int i0 = PAIR == kWhole ? i : 2 * i, i1 = PAIR == kWhole ? i + 8 : 2 * i + 1;
+      const int j = PAIR == kWhole ? 8 * R.e + i : 4 * R.e + (i & 3) + 32 * (i >> 2);
+      if (j < half) {
+        double s64, c64;
+        sincospi(angle_pi(tab.f_pi[j], R.pos), &s64, &c64);
+        c64 *= tab.mag;
+        s64 *= tab.mag;
+        const double x = (double)Elem<T>::get(k, (i0 & 7) + 64 * (i0 >> 3)), p = (double)Elem<T>::get(k, (i1 & 7) + 64 * (i1 >> 3));
+        z[i0] = x * c64 - p * s64;
+        z[i1] = x * s64 + p * c64;
+      }
+    }
+  } else if (PAIR == kFetch) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int d = 8 * R.e + (i & 7) + 64 * (i >> 3);
+      if (d < tab.rot) {
+        double s64, c64;
+        sincospi(angle_pi(tab.f_pi[d < half ? d : d - half], R.pos), &s64, &c64);
+        const double p = (double)Elem<T>::get(static_cast<const T*>(R.k), d < half ? d + half : d - half);
+        z[i] = z[i] * (c64 * tab.mag) + p * ((d < half ? -s64 : s64) * tab.mag);
+      }
+    }
+  }
+  double km = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) km = fabs(z[i]) <= 3.4028235e38 ? fmax(km, fabs(z[i])) : inf;   // once infinite, it stays
+  km = shfl_max(R.mask, km, 4);
+  const float ks = exact_scale(km);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) reinterpret_cast<unsigned*>(R.block + R.r * kRow4)[R.e + 8 * h] = exact_codes(z + 8 * h, ks, ks);
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    z[i] = (double)Elem<T>::get(v, (i & 7) + 64 * (i >> 3));
+    float& m = (i & 4) ? m1 : m0;
+    m = fabs(z[i]) <= 3.4028235e38 ? fmaxf(m, (float)fabs(z[i])) : INFINITY;
+  }
+#pragma unroll
+  for (int o = 2; o <= 4; o <<= 1) {
+    m0 = shfl_max(R.mask, m0, o);
+    m1 = shfl_max(R.mask, m1, o);
+  }
+  const float vs0 = exact_scale(m0), vs1 = exact_scale(m1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    reinterpret_cast<unsigned*>(R.block + kBlockTok * kRow4 + R.r * kRow4)[R.e + 8 * h] = exact_codes(z + 8 * h, vs0, vs1);
+  store_scales(R, ks, vs0, vs1);
+}
+
+// Whether the bf16 scale s of u = amax / 7 (float32) may be another for an amax that is off by err.
+__device__ __forceinline__ bool scale_unsure(float u, float s, float err) {
+  const float half_step = __uint_as_float((__float_as_uint(u) & 0x7f800000u) - (8u << 23));
+  return !(fabsf(fabsf(u - s) - half_step) > fmaf(err, kSeventh, 2.5e-7f * u));
+}
+// Code bits of 8 values, and how far the quotients are from integers.
+__device__ __forceinline__ void round8(const float (&y)[8], float i0, float i1, float (&t)[8], float& far) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = y[i] * (i < 4 ? i0 : i1);
+    t[i] = q + kMagic;
+    far = fmaxf(far, fabsf(q - (t[i] - kMagic)));
+  }
+}
+
+template <typename T, int FMT, int PAIR>
+__global__ void __launch_bounds__(256, 2) k_page_append(const PagePool P, const AppendArgs a, const __grid_constant__ RopeTab128 tab) {
+  const int lane = threadIdx.x & 31;
+  RowPair R;
+  R.e = lane & 7;
+  R.mask = 0xffu << (lane & 24);
+  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3;
+  int hg, b, t;
+  if (item >= (int64_t)a.B * a.T * a.head_groups) return;
+  if (a.small) {   // 32-bit divisions where they suffice
+    const unsigned tok = (unsigned)item / (unsigned)a.head_groups;
+    hg = (int)((unsigned)item - tok * a.head_groups);
+    b = (int)(tok / (unsigned)a.T);
+    t = (int)(tok - (unsigned)b * a.T);
+  } else {
+    const int64_t tok = item / a.head_groups;
+    hg = (int)(item - tok * a.head_groups);
+    b = (int)(tok / a.T);
+    t = (int)(tok - (int64_t)b * a.T);
+  }
+  if (t >= row_count(a.n_new, b, a.T, P.err)) return;
+  const int64_t pos = a.start[b] + t;
+  int blk;
+  unsigned char* const page = page_of(P, b, pos, blk, R.r);
+  if (!page) return;
+  R.pos = (double)pos;
+  const int half = tab.rot / 2;
+  const float mag = (float)tab.mag;
+
+  // cosines and sines: kInLane pairs 4 e + i of the first 8 dims and 32 further; kWhole pairs 8 e + i; kFetch each dim's
+  constexpr int kAngles = PAIR == kNone ? 1 : PAIR == kFetch ? 16 : 8;
+  float c[kAngles], sn[kAngles];
+  if (PAIR != kNone) {
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {
+      const int j = PAIR == kInLane ? 4 * R.e + (i & 3) + 32 * (i >> 2) : PAIR == kWhole ? 8 * R.e + i : 8 * R.e + (i & 7) + 64 * (i >> 3);
       c[i] = 1.f;
       sn[i] = 0.f;
-      if (d < tab.rot) {
-        rope_cs(tab.f_pi[d < half ? d : d - half], (double)pos, mag, c[i], sn[i]);
-        if (d < half) sn[i] = -sn[i];
+      if (PAIR == kFetch) {
+        if (j < tab.rot) {
+          rope_cs(tab.f_pi[j < half ? j : j - half], R.pos, mag, c[i], sn[i]);
+          if (j < half) sn[i] = -sn[i];
+        }
+      } else if (PAIR == kWhole || j < half) {
+        rope_cs(tab.f_pi[j], R.pos, mag, c[i], sn[i]);
       }
     }
   }
   const T* krow = static_cast<const T*>(a.k) + b * a.ks.b + t * a.ks.t;
   const T* vrow = static_cast<const T*>(a.v) + b * a.vs.b + t * a.vs.t;
 
+  Dims<T> kn[2], vn[2];   // the next head's rows, under way while this one's are rounded
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    kn[h].load(krow + hg * a.ks.h + 8 * R.e + 64 * h);
+    vn[h].load(vrow + hg * a.vs.h + 8 * R.e + 64 * h);
+  }
   for (int g = hg; g < P.Hkv; g += a.head_groups) {
-    float x[8], p[8], y[8], v[8];
     const T* kh = krow + g * a.ks.h;
-    load8(kh + 8 * e, x);
-    load8(vrow + g * a.vs.h + 8 * e, v);
+    const T* vh = vrow + g * a.vs.h;
+    Dims<T> kd[2], vd[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = 0.f;
-    if (PAIR == kInLane) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (8 * e + i < tab.rot) p[i] = x[i ^ 1];
-    } else if (PAIR == kShuffle) {
-      const int n8 = half / 8, src = e < n8 ? e + n8 : e - n8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = __shfl_sync(mask, x[i], (lane & 16) + (src & 15));
-        if (turned) p[i] = w;
-      }
-    } else if (PAIR == kReload) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = 8 * e + i;
-        if (d < tab.rot) p[i] = Elem<T>::get(kh, d < half ? d + half : d - half);
+    for (int h = 0; h < 2; ++h) {
+      kd[h] = kn[h];
+      vd[h] = vn[h];
+      if (g + a.head_groups < P.Hkv) {
+        kn[h].load(kh + a.head_groups * a.ks.h + 8 * R.e + 64 * h);
+        vn[h].load(vh + a.head_groups * a.vs.h + 8 * R.e + 64 * h);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = PAIR == kNone ? x[i] : fmaf(x[i], c[i], p[i] * sn[i]);
-
-    unsigned char* const blkp = page + (size_t)g * P.head_bytes + (size_t)blk * (FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16);
-    if (FMT == kPageBf16) {
-      // the cache keeps 16 bits: one rounding of the float32 rotation
-      *reinterpret_cast<uint4*>(blkp + r * 256 + ((e ^ (r & 7)) << 4)) = pack8(y);
-      *reinterpret_cast<uint4*>(blkp + kBlockTok * 256 + r * 256 + ((e ^ (r & 7)) << 4)) = pack8(v);
-      continue;
-    }
-    // ---- group maxima of |K| (as bit patterns, so that NaN is above infinity) and |V|
-    unsigned kb = 0u, v0 = 0u, v1 = 0u;
-    float off = 0.f;   // bound of the float32 rotation's error over the group
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      kb = max(kb, __float_as_uint(y[i]) & 0x7fffffffu);
-      const unsigned w = __float_as_uint(v[i]) & 0x7fffffffu;
-      if (i < 4) v0 = max(v0, w);
-      else v1 = max(v1, w);
-      // cos and sin are off by at most 1.6e-7 (argument and function) and 6e-8 (magnitude), the
-      // products and the sum by 6e-8 each
-      if (PAIR != kNone) off = fmaxf(off, (fabsf(x[i]) + fabsf(p[i])));
-    }
-#pragma unroll
-    for (int o = 4; o <= 8; o <<= 1) {
-      kb = shfl_max(mask, kb, o);
-      if (PAIR != kNone) off = shfl_max(mask, off, o);
-    }
-#pragma unroll
-    for (int o = 2; o <= 8; o <<= 1) {
-      v0 = shfl_max(mask, v0, o);
-      v1 = shfl_max(mask, v1, o);
-    }
-    off *= 5e-7f * fmaxf(mag, 1.f);
-    const float amax = __uint_as_float(kb);
-    float ks = group_scale(amax);
-    const float vs0 = group_scale(__uint_as_float(v0)), vs1 = group_scale(__uint_as_float(v1));
-    unsigned kw = 0u, vw = 0u;
-    bool plain = ks > 0.f;   // a scale of 0 or NaN goes with code 8 everywhere
-    const float ki = plain ? 1.f / ks : 0.f;
-    if (PAIR == kNone) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) kw |= (plain ? code_exact(y[i], ks, ki) : 8u) << (4 * i);
-    } else {
-      // near: a border of the scale's or of a code's rounding lies within the error
-      bool near = plain && (group_scale(amax + off) != ks || group_scale(fmaxf(amax - off, 0.f)) != ks);
-      const float lim = off * ki + 2e-6f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = y[i] * ki, n = rintf(q);
-        near |= plain && 0.5f - fabsf(q - n) < lim;
-        kw |= (plain ? (unsigned)((int)fminf(fmaxf(n, -7.f), 7.f) + 8) : 8u) << (4 * i);
-      }
-      if (__any_sync(mask, near)) {   // the row again in 64 bits
-        double z[8], am = 0.0;
+    float y[2][8];
+    unsigned xtop = 0u;   // float bits of the largest |x| + |partner|
+    {
+      float x[2][8];
+      kd[0].get(x[0]);
+      kd[1].get(x[1]);
+      const float top0 = __uint_as_float(FMT == kPageInt4 && PAIR != kNone ? kd[0].top() : 0u);
+      const float top1 = __uint_as_float(FMT == kPageInt4 && PAIR != kNone ? kd[1].top() : 0u);
+      if (PAIR == kNone) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int d = 8 * e + i;
-          z[i] = (double)x[i];
-          if (d < tab.rot) {
-            const int j = PAIR == kInLane ? d >> 1 : d < half ? d : d - half;
-            double s64, c64;
-            sincospi(angle_pi(tab.f_pi[j], (double)pos), &s64, &c64);
-            if (PAIR == kInLane ? !(i & 1) : d < half) s64 = -s64;
-            z[i] = (double)x[i] * (c64 * tab.mag) + (double)p[i] * (s64 * tab.mag);
-          }
-          am = fmax(am, fabs(z[i]));
+          y[0][i] = x[0][i];
+          y[1][i] = x[1][i];
         }
-        am = shfl_max(mask, am, 4);
-        am = shfl_max(mask, am, 8);
-        if (plain) {
-          ks = seventh(am);
-          kw = 0u;
+      } else if (PAIR == kWhole) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            kw |= (unsigned)((int)fmin(fmax(rint(z[i] / (double)ks), -7.0), 7.0) + 8) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+          const int j = i % kAngles;
+          y[0][i] = fmaf(x[0][i], c[j], -x[1][i] * sn[j]);
+          y[1][i] = fmaf(x[1][i], c[j], x[0][i] * sn[j]);
         }
+        xtop = __float_as_uint(top0 + top1);
+      } else if (PAIR == kInLane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = (4 * h + i) % kAngles;
+            // dims that do not turn stay out of it: their neighbours may be infinite
+            const bool turns = 8 * R.e + 64 * h + 2 * i < tab.rot;
+            const float u = x[h][2 * i], w = x[h][2 * i + 1];
+            y[h][2 * i] = turns ? fmaf(u, c[j], -w * sn[j]) : u;
+            y[h][2 * i + 1] = turns ? fmaf(w, c[j], u * sn[j]) : w;
+          }
+        xtop = max(__float_as_uint(top0 + top0), __float_as_uint(top1 + top1));
+      } else {
+        float most = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = 8 * R.e + i + 64 * h, j = (8 * h + i) % kAngles;
+            y[h][i] = x[h][i];
+            float sum = fabsf(x[h][i]);
+            if (d < tab.rot) {
+              const float p = Elem<T>::get(kh, d < half ? d + half : d - half);
+              y[h][i] = fmaf(x[h][i], c[j], p * sn[j]);
+              sum += fabsf(p);
+            }
+            nan = nan || !(sum <= 3.4028235e38f);
+            most = fmaxf(most, sum);
+          }
+        xtop = nan ? 0x7fc00000u : __float_as_uint(most);
       }
     }
-    const float vi0 = vs0 > 0.f ? 1.f / vs0 : 0.f, vi1 = vs1 > 0.f ? 1.f / vs1 : 0.f;
+    R.block = page + (size_t)g * P.head_bytes + (size_t)blk * (FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16);
+    float v[2][8];
+    vd[0].get(v[0]);
+    vd[1].get(v[1]);
+    if (FMT == kPageBf16) {
+      // the cache keeps 16 bits: one rounding of the float32 rotation
+      unsigned char* const to = R.block + R.r * 256 + ((R.e ^ (R.r & 7)) << 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = i < 4 ? vs0 : vs1, inv = i < 4 ? vi0 : vi1;
-      vw |= (s > 0.f ? code_exact(v[i], s, inv) : 8u) << (4 * i);
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<uint4*>(to + 128 * h) = pack8(y[h]);
+        *reinterpret_cast<uint4*>(to + kBlockTok * 256 + 128 * h) = pack8(v[h]);
+      }
+      continue;
     }
-    reinterpret_cast<unsigned*>(blkp + r * kRow4)[e] = kw;
-    reinterpret_cast<unsigned*>(blkp + kBlockTok * kRow4 + r * kRow4)[e] = vw;
-    // scales: K group g in lane g; V groups 0, 1 in lane 0 and 2, 3 in lane 1
-    unsigned char* const sc = blkp + 2 * kBlockTok * kRow4 + r * 16;
-    if (e < 4) reinterpret_cast<unsigned short*>(sc)[e] = (unsigned short)(__float_as_uint(ks) >> 16);
-    if (e < 2) reinterpret_cast<unsigned*>(sc + 8)[e] = (__float_as_uint(vs0) >> 16) | (__float_as_uint(vs1) & 0xffff0000u);
+    // ---- K: the lane's 16 dims are of scale group e % 4, shared with lane e ^ 4.
+    // V: dims 4 further are of the next group than 2 (e % 2), both shared with the lanes of e's parity.
+    unsigned ktop, v0, v1;   // float bits of the groups' largest magnitudes
+    if (PAIR == kNone) {
+      ktop = max(kd[0].top(), kd[1].top());
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(y[0][i]), fabsf(y[1][i])));
+      ktop = __float_as_uint(m);
+      xtop = shfl_max(R.mask, xtop, 4);
+    }
+    ktop = shfl_max(R.mask, ktop, 4);
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t m0 = max_u16x2(vd[0].top2(0), vd[1].top2(0)), m1 = max_u16x2(vd[0].top2(2), vd[1].top2(2));
+      uint32_t m = max_u16x2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));   // group low, group high
+#pragma unroll
+      for (int o = 2; o <= 4; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(R.mask, m, o));
+      v0 = m << 16;
+      v1 = m & 0xffff0000u;
+    } else {
+      v0 = max(vd[0].top4(0), vd[1].top4(0));
+      v1 = max(vd[0].top4(4), vd[1].top4(4));
+#pragma unroll
+      for (int o = 2; o <= 4; o <<= 1) {
+        v0 = shfl_max(R.mask, v0, o);
+        v1 = shfl_max(R.mask, v1, o);
+      }
+    }
+    bool unsure = odd_group(ktop) || odd_group(v0) || odd_group(v1);
+    const float ku = __uint_as_float(ktop) * kSeventh, vu0 = __uint_as_float(v0) * kSeventh, vu1 = __uint_as_float(v1) * kSeventh;
+    const float ks = bf16_of(ku), vs0 = bf16_of(vu0), vs1 = bf16_of(vu1);
+    const float ki = rcp(ks), vi0 = rcp(vs0), vi1 = rcp(vs1);
+    unsigned kw[2], vw[2];
+    // bf16 rows as given: exact by round4 (and the scale of 8 bits likewise)
+    if (sizeof(T) == 2 && PAIR == kNone) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q[8];
+        round4(y[h], ks, ki, q);
+        round4(y[h] + 4, ks, ki, q + 4);
+        kw[h] = pack_codes(q);
+      }
+    } else {
+      // A rotated value is off by at most 5e-7 m (|x| + |partner|): cos and sin by 1.6e-7 (argument and function)
+      // and 6e-8 (magnitude), the products and the sum by 6e-8 each.  NaN and infinity show here, too.
+      const float err = PAIR == kNone ? 0.f : __uint_as_float(xtop) * (5e-7f * fmaxf(mag, 1.f));
+      float far = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q[8];
+        round8(y[h], ki, ki, q, far);
+        kw[h] = pack_codes(q);
+      }
+      // a border of a code's rounding, or of the scale's, within the error of the value and of the quotient
+      unsure = unsure || !(0.5f - far > fmaf(err, ki, 2e-6f)) || scale_unsure(ku, ks, err);
+    }
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q[8];
+        round4(v[h], vs0, vi0, q);
+        round4(v[h] + 4, vs1, vi1, q + 4);
+        vw[h] = pack_codes(q);
+      }
+    } else {
+      float far = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q[8];
+        round8(v[h], vi0, vi1, q, far);
+        vw[h] = pack_codes(q);
+      }
+      unsure = unsure || !(0.5f - far > 2e-6f) || scale_unsure(vu0, vs0, 0.f) || scale_unsure(vu1, vs1, 0.f);
+    }
+    if (__any_sync(R.mask, unsure)) {
+      R.k = kh;
+      R.v = vh;
+      store_exact<T, PAIR>(R, tab);
+      continue;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      reinterpret_cast<unsigned*>(R.block + R.r * kRow4)[R.e + 8 * h] = kw[h];
+      reinterpret_cast<unsigned*>(R.block + kBlockTok * kRow4 + R.r * kRow4)[R.e + 8 * h] = vw[h];
+    }
+    store_scales(R, ks, vs0, vs1);
   }
 }
 
@@ -373,8 +599,8 @@ template <typename T, int FMT>
 cudaError_t append_go(const PagePool& pool, const AppendArgs& a, const RopeTab128& tab, unsigned blocks, cudaStream_t st) {
   if (tab.rot == 0) k_page_append<T, FMT, kNone><<<blocks, 256, 0, st>>>(pool, a, tab);
   else if (tab.interleaved) k_page_append<T, FMT, kInLane><<<blocks, 256, 0, st>>>(pool, a, tab);
-  else if (tab.rot % 16 == 0) k_page_append<T, FMT, kShuffle><<<blocks, 256, 0, st>>>(pool, a, tab);
-  else k_page_append<T, FMT, kReload><<<blocks, 256, 0, st>>>(pool, a, tab);
+  else if (tab.rot == kHeadDim) k_page_append<T, FMT, kWhole><<<blocks, 256, 0, st>>>(pool, a, tab);
+  else k_page_append<T, FMT, kFetch><<<blocks, 256, 0, st>>>(pool, a, tab);
   return cudaGetLastError();
 }
 
@@ -385,9 +611,10 @@ cudaError_t launch_page_append(const PagePool& pool, AppendArgs a, int dtype, in
   // A thread takes up to 8 heads of its token, fewer while the GPU would not be full.
   const int64_t toks = (int64_t)a.B * a.T;
   a.head_groups = (pool.Hkv + 7) / 8;
-  while (a.head_groups < pool.Hkv && toks * a.head_groups * 16 < (int64_t)num_sms * 1024) a.head_groups *= 2;
+  while (a.head_groups < pool.Hkv && toks * a.head_groups * 8 < (int64_t)num_sms * 512) a.head_groups *= 2;
   if (a.head_groups > pool.Hkv) a.head_groups = pool.Hkv;
-  const int64_t blocks = (toks * a.head_groups * 16 + 255) / 256;
+  const int64_t blocks = (toks * a.head_groups * 8 + 255) / 256;
+  a.small = toks * a.head_groups < INT32_MAX;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (dtype == 0)
     return format == kPageInt4 ? append_go<__nv_bfloat16, kPageInt4>(pool, a, tab, (unsigned)blocks, st)

@@ -95,7 +95,7 @@ struct RopeArgs {
   int64_t items;              // B * T * head_groups * chunks of a row
   int T, H, d;
   int head_groups;
-  int n_rot, n_copy;          // chunks of a row that turn, and that are copied
+  int n_rot, n_copy;          // threads of a row whose chunks turn, and are copied
   float sign;                 // -1: transposed
 };
 
@@ -129,65 +129,73 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a, const __grid_con
   const T* x = static_cast<const T*>(a.x) + b * a.xs.b + t * a.xs.t;
   T* y = static_cast<T*>(a.y) + b * a.ys.b + t * a.ys.t;
 
-  if (j >= a.n_rot) {   // a chunk past the rotated dims
-    const int d0 = tab.rot + (j - a.n_rot) * V;
-    for (int h = hg; h < a.H; h += a.head_groups) {
-      Chunk<T, V> c;
-      c.load(x + h * a.xs.h + d0);
-      c.store(y + h * a.ys.h + d0);
-    }
-    return;
-  }
-  const double pos = (double)(a.positions ? a.positions[(int64_t)b * a.T + t] : a.start[b] + t);
+  // A chunk past the rotated dims goes the same way (a warp holds both kinds), its bits as they are.
+  const bool turns = j < a.n_rot;
   float c[kPairs], s[kPairs];
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    rope_cs(tab.f_pi[j * kPairs + i], pos, (float)tab.mag, c[i], s[i]);
-    s[i] *= a.sign;
+  for (int i = 0; i < kPairs; ++i) c[i] = s[i] = 0.f;
+  if (turns) {
+    const double pos = (double)(a.positions ? a.positions[(int64_t)b * a.T + t] : a.start[b] + t);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      rope_cs(tab.f_pi[j * kPairs + i], pos, (float)tab.mag, c[i], s[i]);
+      s[i] *= a.sign;
+    }
   }
   // offsets of the chunk's first and second load
-  const int d0 = INTER ? (V == 1 ? 2 * j : j * V) : j * V;
-  const int d1 = INTER ? 2 * j + 1 : tab.rot / 2 + j * V;
   constexpr bool kTwo = !INTER || V == 1;
+  int d0 = INTER ? (V == 1 ? 2 * j : j * V) : j * V;
+  int d1 = INTER ? 2 * j + 1 : tab.rot / 2 + j * V;
+  bool two = kTwo;
+  if (!turns) {
+    d0 = tab.rot + (j - a.n_rot) * (kTwo ? 2 * V : V);
+    d1 = d0 + V;
+    two = kTwo && d1 < a.d;
+  }
   constexpr int U = 4;   // heads in flight
+  const int64_t xstep = a.head_groups * a.xs.h, ystep = a.head_groups * a.ys.h;
+  x += hg * a.xs.h;
+  y += hg * a.ys.h;
   for (int h0 = hg; h0 < a.H; h0 += U * a.head_groups) {
     Chunk<T, V> p0[U], p1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * a.head_groups;
-      if (h < a.H) {
-        p0[u].load(x + h * a.xs.h + d0);
-        if (kTwo) p1[u].load(x + h * a.xs.h + d1);
+      if (h0 + u * a.head_groups < a.H) {
+        p0[u].load(x + u * xstep + d0);
+        if (two) p1[u].load(x + u * xstep + d1);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * a.head_groups;
-      if (h < a.H) {
-        float f0[V], f1[V];
-        p0[u].get(f0);
-        if (kTwo) {
-          p1[u].get(f1);
+      if (h0 + u * a.head_groups < a.H) {
+        if (turns) {
+          float f0[V], f1[V];
+          p0[u].get(f0);
+          if (kTwo) {
+            p1[u].get(f1);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float u0 = f0[i], v0 = f1[i];
-            f0[i] = u0 * c[i] - v0 * s[i];
-            f1[i] = u0 * s[i] + v0 * c[i];
-          }
-          p1[u].set(f1);
-          p1[u].store(y + h * a.ys.h + d1);
-        } else {
+            for (int i = 0; i < V; ++i) {
+              const float u0 = f0[i], v0 = f1[i];
+              f0[i] = u0 * c[i] - v0 * s[i];
+              f1[i] = u0 * s[i] + v0 * c[i];
+            }
+            p1[u].set(f1);
+          } else {
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            const float u0 = f0[2 * i], v0 = f0[2 * i + 1];
-            f0[2 * i] = u0 * c[i] - v0 * s[i];
-            f0[2 * i + 1] = u0 * s[i] + v0 * c[i];
+            for (int i = 0; i < V / 2; ++i) {
+              const float u0 = f0[2 * i], v0 = f0[2 * i + 1];
+              f0[2 * i] = u0 * c[i] - v0 * s[i];
+              f0[2 * i + 1] = u0 * s[i] + v0 * c[i];
+            }
           }
+          p0[u].set(f0);
         }
-        p0[u].set(f0);
-        p0[u].store(y + h * a.ys.h + d0);
+        p0[u].store(y + u * ystep + d0);
+        if (two) p1[u].store(y + u * ystep + d1);
       }
     }
+    x += U * xstep;
+    y += U * ystep;
   }
 }
 
@@ -195,7 +203,8 @@ template <typename T, int V>
 cudaError_t go(RopeArgs a, int B, const RopeTabAny& tab, cudaStream_t st) {
   const bool inter = tab.interleaved != 0;
   a.n_rot = inter ? tab.rot / (V == 1 ? 2 : V) : tab.rot / 2 / V;
-  a.n_copy = (a.d - tab.rot) / V;
+  const int two = inter && V > 1 ? 1 : 2;   // chunks a thread copies
+  a.n_copy = ((a.d - tab.rot) / V + two - 1) / two;
   a.items = (int64_t)B * a.T * a.head_groups * (a.n_rot + a.n_copy);
   const int64_t blocks = (a.items + 255) / 256;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;

@@ -69,6 +69,7 @@ struct AppendArgs {
   const int64_t* n_new;    // optional
   int B, T;
   int head_groups;         // a thread takes the heads h, h + head_groups, ...
+  int small;               // B * T * head_groups fits 31 bits
 };
 
 struct ReadArgs {
