@@ -215,6 +215,12 @@ struct Rows {
 };
 constexpr unsigned kList = 0x10000u;
 
+constexpr int kMergeWords = 9 * 32 * 4;   // a warp's state as its lanes hold it: 32 sums, maximum and sum
+
+// Rotated queries in shared memory: the dims 32 apart of 8 heads fall into 32 banks.
+constexpr int kQRow = 161;
+__device__ __forceinline__ int q_at(int d) { return d + 8 * (d >> 5); }
+
 // W warps, items of U units (4 bits 2, bf16 1), S ring slots a warp; WIDE: more than 4 heads a group (bf16 only, see the matrix mapping); LISTED: a
 // selection is given.
 template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
@@ -225,15 +231,16 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   static_assert(U == (kF16 ? 2 : 1), "items of each format");
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* const ring = smem;                                              // [W][S][U][kBlk]
-  float* const mbuf = reinterpret_cast<float*>(smem + (size_t)W * S * U * kBlk);     // [(W + 1) / 2][8][kPartStride]
-  float* const cbuf = mbuf + (W + 1) / 2 * kMaxGroup * kPartStride;              // [max(W, 8)][kPartStride]
-  float* const qs = cbuf + (W > kMaxGroup ? W : kMaxGroup) * kPartStride;        // [8][128]
-  long long* const rpre = reinterpret_cast<long long*>(qs + kMaxGroup * kHeadDim);  // [n_slices + 1]
+  float* const mbuf = reinterpret_cast<float*>(smem + (size_t)W * S * U * kBlk);     // [(W + 1) / 2][kMergeWords]
+  float* const cbuf = mbuf + (W + 1) / 2 * kMergeWords;              // [max(W, 8)][kPartStride]
+  float* const qs = cbuf + (W > kMaxGroup ? W : kMaxGroup) * kPartStride;        // [8][kQRow]
+  long long* const rpre = reinterpret_cast<long long*>(qs + kMaxGroup * kQRow);  // [n_slices + 1]
   int2* const sinfo = reinterpret_cast<int2*>(rpre + A.n_slices + 1);            // [n_slices] (L, listed rows)
   __shared__ __align__(8) unsigned long long full[W * S];
   __shared__ unsigned vmask[W * S * U];   // attended rows of a slot's units; bit 16: gathered
   __shared__ long long shl[W];
   __shared__ int s_merge;
+  __shared__ float qtop[kMaxGroup];
   __shared__ uint4 qf[kF16 ? 8 * 32 : 1];      // 4 bits: query operands, a lane's 16 bytes of each k-step
   __shared__ float2 q8[kF16 ? 4 * 8 : 1];      // 4 bits: -8 times a scale group's sum of queries (high, residual), each head
   __shared__ __align__(16) float kscale[kF16 ? 4 * W * 32 : 4];   // 4 bits, of the item in hand: scales of K, by group and row
@@ -247,8 +254,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
   // ---- item prefix over slices
+  bool whole;
   {
     long long carry = 0;
+    bool big = false;
     for (int base = 0; base < NS; base += W * 32) {
       const int s = base + tid;
       long long n = 0;
@@ -269,6 +278,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         }
         sinfo[s] = make_int2((int)L, cnt);
         n = (units_of(make_slice(A, g, (int)L, cnt)) + U - 1) / U;
+        big = big || n > 2 * W;
       }
       long long v = n;
 #pragma unroll
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       __syncthreads();
     }
     if (tid == 0) rpre[NS] = carry;
-    __syncthreads();
+    whole = !__syncthreads_or(big) && NS <= (int)gridDim.x;
   }
   const long long T = rpre[NS];
   // slices without a row: zeros
@@ -300,11 +310,20 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     for (int i = tid; i < G * kHeadDim; i += W * 32) A.out[h0 * kHeadDim + i] = 0.f;
     if (A.lse && tid < G) A.lse[h0 + tid] = -INFINITY;
   }
-  // every active CTA has at least one item a warp
-  const long long want = (T + W - 1) / W;
-  const int nb = (long long)gridDim.x < want ? (int)gridDim.x : (int)want;
-  if ((int)blockIdx.x >= nb) return;
-  const long long r_lo = (long long)blockIdx.x * T / nb, r_hi = (long long)(blockIdx.x + 1) * T / nb;
+  // Equal shares, down to one item a CTA.  Where there are CTAs enough and no slice has more than two items a
+  // warp, a CTA takes one slice: nothing is left to merge between CTAs.
+  long long r_lo, r_hi;
+  const int nb = (long long)gridDim.x < T ? (int)gridDim.x : (int)T;
+  if (whole) {
+    if ((int)blockIdx.x >= NS) return;
+    r_lo = rpre[blockIdx.x];
+    r_hi = rpre[blockIdx.x + 1];
+    if (r_lo == r_hi) return;
+  } else {
+    if ((int)blockIdx.x >= nb) return;
+    r_lo = (long long)blockIdx.x * T / nb;
+    r_hi = (long long)(blockIdx.x + 1) * T / nb;
+  }
   auto owner = [&](long long r) { return (int)(((r + 1) * nb - 1) / T); };
   auto slice_of = [&](long long r) {
     int lo = 0, hi = NS - 1;
@@ -502,8 +521,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         }
         float c = 1.f, sn = 0.f;
         if (j < half) rope_cs(tab.f_pi[j], (double)pos, (float)tab.mag, c, sn);
-        qs[h * kHeadDim + d0] = (q0 * c - q1 * sn) * A.scale_log2;
-        qs[h * kHeadDim + d1] = (q0 * sn + q1 * c) * A.scale_log2;
+        qs[h * kQRow + q_at(d0)] = (q0 * c - q1 * sn) * A.scale_log2;
+        qs[h * kQRow + q_at(d1)] = (q0 * sn + q1 * c) * A.scale_log2;
       }
       __syncthreads();
     }
@@ -513,15 +532,19 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     uint32_t qb[WIDE ? 8 : 1][2];   // the low part's rows where they need a product of their own
     float unscale = 1.f;
     if (kF16) {
-      const float* q = qs + (gid < G ? gid : 0) * kHeadDim + 32 * t4;
-      float top = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(q[i]));
-      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      for (int h = warp; h < G; h += W) {   // the heads' largest components
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(qs[h * kQRow + q_at(lane + 32 * k)]));
+        top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+        if (lane == 0) qtop[h] = top;
+      }
+      __syncthreads();
+      const float top = qtop[gid < G ? gid : 0];
       const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
       const float f = gid < G ? __uint_as_float((unsigned)(127 + 10 - e) << 23) : 0.f;
       unscale = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kCodeUnit;
+      const float* q = qs + (gid < G ? gid : 0) * kQRow + q_at(32 * t4);
       for (int kk = warp; kk < 8; kk += W) {
         const float* x = q + 8 * (kk >> 1) + 2 * (kk & 1);
         __half2 h[2], lo[2];
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       const bool in = h < G;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        const float* x = qs + (in ? h : 0) * kHeadDim + 16 * kk + 2 * t4;
+        const float* x = qs + (in ? h : 0) * kQRow + q_at(16 * kk) + 2 * t4;
         uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) split_bf16(in ? x[8 * i] : 0.f, in ? x[8 * i + 1] : 0.f, hi[i], mid[i], lo[i]);
@@ -828,40 +851,35 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
             for (int k = 0; k < 4; ++k)
               *reinterpret_cast<float2*>(dst + 8 * (nt + k) + 2 * t4) = make_float2(o[nt + k][0], o[nt + k][1]);
     };
-    auto add = [&](const float* src, float sa, float sb) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int nt = 0; nt < 16; ++nt) {
-          const float v = src[FMT == kPageInt4 ? 32 * t4 + 16 * e + nt : 8 * nt + 2 * t4 + e];
-          o[nt][e] = o[nt][e] * sa + v * sb;
-        }
-    };
 #pragma unroll 1
     for (int n = W; n > 1; n = (n + 1) / 2) {
       const int half = (n + 1) / 2;   // warps half .. n - 1 hand over to 0 ..
-      if (warp >= half && warp < n && gid < G) {
-        float* dst = mbuf + ((size_t)(warp - half) * kMaxGroup + gid) * kPartStride;
-        put(dst);
-        if (t4 == 0) {
-          dst[kHeadDim] = m;
-          dst[kHeadDim + 1] = l;
-        }
+      float4* const box = reinterpret_cast<float4*>(mbuf + (size_t)(warp >= half ? warp - half : warp) * kMergeWords) + lane;
+      if (warp >= half && warp < n) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) box[32 * k] = make_float4(o[2 * k][0], o[2 * k][1], o[2 * k + 1][0], o[2 * k + 1][1]);
+        box[256] = make_float4(m, l, 0.f, 0.f);
       }
       __syncthreads();
-      if (warp < n - half && gid < G) {
-        const float* src = mbuf + ((size_t)warp * kMaxGroup + gid) * kPartStride;
-        const float m2 = src[kHeadDim], l2 = src[kHeadDim + 1];
-        const float mn = fmaxf(m, m2);
-        const float sa = exp2f(m - mn), sb = exp2f(m2 - mn);
-        l = l * sa + l2 * sb;
-        add(src, sa, sb);
+      if (warp < n - half) {
+        const float4 ml = box[256];
+        const float mn = fmaxf(m, ml.x);
+        const float sa = exp2f(m - mn), sb = exp2f(ml.x - mn);
+        l = l * sa + ml.y * sb;
         m = mn;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 v = box[32 * k];
+          o[2 * k][0] = o[2 * k][0] * sa + v.x * sb;
+          o[2 * k][1] = o[2 * k][1] * sa + v.y * sb;
+          o[2 * k + 1][0] = o[2 * k + 1][0] * sa + v.z * sb;
+          o[2 * k + 1][1] = o[2 * k + 1][1] * sa + v.w * sb;
+        }
       }
       __syncthreads();
     }
     // ---- alone on the slice: the output; else its state, and the last CTA merges them
-    const int c0 = owner(rpre[s]), c1 = owner(rpre[s + 1] - 1);
+    const int c0 = whole ? 0 : owner(rpre[s]), c1 = whole ? 0 : owner(rpre[s + 1] - 1);
     if (warp == 0 && gid < G) {
       float* dst;
       if (c0 == c1) {
@@ -962,7 +980,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
 template <int FMT, int W, int U, int S>
 constexpr size_t smem_bytes(int n_slices) {
   const size_t blk = FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
-  return W * U * S * blk + (size_t)((W + 1) / 2 * kMaxGroup + (W > kMaxGroup ? W : kMaxGroup)) * kPartStride * 4 + kMaxGroup * kHeadDim * 4 +
+  return W * U * S * blk + (size_t)((W + 1) / 2 * kMergeWords + (W > kMaxGroup ? W : kMaxGroup) * kPartStride) * 4 + kMaxGroup * kQRow * 4 +
          (size_t)(n_slices + 1) * 8 + (size_t)n_slices * 8;
 }
 constexpr size_t smem_most(int format) { return (format == kPageInt4 ? 212 : 226) * 1024; }   // 227 KB less the static arrays
