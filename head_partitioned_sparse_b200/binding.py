@@ -13,6 +13,7 @@ module raises on first use.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -421,22 +422,49 @@ def spa_select_noalloc(P_q, n_q_heads: int, n_kv_heads: int, kv_dtype: int, idx_
 
 # ---- rotary positions and the paged cache
 
-def _dev(x) -> Optional[int]:
+# These calls take a few microseconds on the GPU in a decode step, so the marshalling is kept short: the current
+# device and its stream are asked for once a call, strides are converted once a value.
+
+def _device() -> int:
+    """The current CUDA device, -1 without one."""
+    global _torch_cuda
+    if _torch_cuda is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -1
+        torch.cuda.init()
+        _torch_cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _torch_cuda[0]()
+
+
+_torch_cuda = None
+
+
+def _dev(x, device: int) -> Optional[int]:
     """_ptr of a tensor that a kernel reads: a host tensor, or one of another device than the
     current one, is refused (its address would fault on the GPU)."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     d = x.get_device()
-    if d < 0:
-        raise ValueError("expected a CUDA tensor, got one in host memory")
-    import torch
-    if d != torch.cuda.current_device():
-        raise ValueError(f"tensor on device {d}, the current device is {torch.cuda.current_device()}")
+    if d != device or d < 0:
+        raise ValueError("expected a CUDA tensor, got one in host memory" if d < 0 else
+                         f"tensor on device {d}, the current device is {device}")
     return x.data_ptr()
 
 
+def _on(s, device: int) -> Optional[int]:
+    if s is None:
+        return _torch_cuda[1](device) if device >= 0 else None
+    return s if s.__class__ is int else s.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _stride_array(s):
+    return (ctypes.c_int64 * 3)(*s)
+
+
 def _strides(s):
-    return None if s is None else (ctypes.c_int64 * 3)(*s)
+    return None if s is None else _stride_array(tuple(s))
 
 
 def make_rope_config(*, rot_dim: int = 128, layout: int = SPA_ROPE_HALF, theta: float = 500000.0,
@@ -466,9 +494,12 @@ def spa_rope_inv_freq(r, n: int) -> Tuple[float, ...]:
 def spa_rope_apply(r, x, y, B: int, T: int, n_heads: int, head_dim: int, dtype: int, start_pos=None, positions=None,
                    x_strides=None, y_strides=None, transpose: bool = False, stream=None) -> None:
     """Strides are (batch, token, head) in elements; None is dense [B][n_heads][T][head_dim]."""
-    _check(load().spa_rope_apply(r, _dev(x), _strides(x_strides), _dev(y), _strides(y_strides), _dev(start_pos),
-                                 _dev(positions), B, T, n_heads, head_dim, dtype, 1 if transpose else 0,
-                                 _stream(stream)))
+    d = _device()
+    st = (_lib or load()).spa_rope_apply(r, _dev(x, d), _strides(x_strides), _dev(y, d), _strides(y_strides),
+                                         _dev(start_pos, d), _dev(positions, d), B, T, n_heads, head_dim, dtype,
+                                         1 if transpose else 0, _on(stream, d))
+    if st:
+        _check(st)
 
 
 def make_paged_config(*, max_batch: int, n_q_heads: int, n_kv_heads: int, kv_dtype: int, page_format: int,
@@ -501,24 +532,33 @@ def spa_paged_status(h, stream=None) -> None:
 def spa_kv_append_paged(h, k_pre, v_new, start_pos, B: int, T: int, block_table, pages, n_new=None, k_strides=None,
                         v_strides=None, stream=None) -> None:
     """Strides are (batch, token, head) in elements; None is dense [B][Hkv][T][128]."""
-    _check(load().spa_kv_append_paged(h, _dev(k_pre), _strides(k_strides), _dev(v_new), _strides(v_strides),
-                                      _dev(start_pos), _dev(n_new), B, T, _dev(block_table), _dev(pages),
-                                      _stream(stream)))
+    d = _device()
+    st = (_lib or load()).spa_kv_append_paged(h, _dev(k_pre, d), _strides(k_strides), _dev(v_new, d),
+                                              _strides(v_strides), _dev(start_pos, d), _dev(n_new, d), B, T,
+                                              _dev(block_table, d), _dev(pages, d), _on(stream, d))
+    if st:
+        _check(st)
 
 
 def spa_kv_read_paged(h, pages, block_table, start_pos, B: int, T: int, k_rows, v_rows, n_rows=None, k_strides=None,
                       v_strides=None, stream=None) -> None:
     """Strides are (batch, token, head) in elements; None is dense [B][Hkv][T][128]."""
-    _check(load().spa_kv_read_paged(h, _dev(pages), _dev(block_table), _dev(start_pos), _dev(n_rows), B, T,
-                                    _dev(k_rows), _strides(k_strides), _dev(v_rows), _strides(v_strides),
-                                    _stream(stream)))
+    d = _device()
+    st = (_lib or load()).spa_kv_read_paged(h, _dev(pages, d), _dev(block_table, d), _dev(start_pos, d),
+                                            _dev(n_rows, d), B, T, _dev(k_rows, d), _strides(k_strides),
+                                            _dev(v_rows, d), _strides(v_strides), _on(stream, d))
+    if st:
+        _check(st)
 
 
 def spa_attend_paged(h, q_pre, pages, block_table, seq_lens, B: int, max_seq_len: int, out, head_mask=None,
                      n_sink: int = 0, window: int = 0, sel_idx=None, sel_count=None, sel_stride: int = 0, lse=None,
                      stream=None) -> None:
     """head_mask: None (every head attends every row), or the host mask [Hkv] (bytes, list or tensor)."""
-    mask = None if head_mask is None else head_mask if isinstance(head_mask, bytes) else _host_u8(head_mask)
-    _check(load().spa_attend_paged(h, _dev(q_pre), _dev(pages), _dev(block_table), _dev(seq_lens), B, max_seq_len,
-                                   mask, n_sink, window, _dev(sel_idx), _dev(sel_count), sel_stride, _dev(out),
-                                   _dev(lse), _stream(stream)))
+    mask = head_mask if head_mask is None or head_mask.__class__ is bytes else _host_u8(head_mask)
+    d = _device()
+    st = (_lib or load()).spa_attend_paged(h, _dev(q_pre, d), _dev(pages, d), _dev(block_table, d), _dev(seq_lens, d),
+                                           B, max_seq_len, mask, n_sink, window, _dev(sel_idx, d), _dev(sel_count, d),
+                                           sel_stride, _dev(out, d), _dev(lse, d), _on(stream, d))
+    if st:
+        _check(st)

@@ -12,7 +12,9 @@
 // bits: K, V and scales together).  Listed units are gathered by 16-byte asynchronous copies, their
 // positions loaded two items ahead, their pages one.
 // (Two producer warps for the whole CTA were measured 1.8 times slower: one lane's waits and copies in turn.)
-// Warps keep their own running maximum and sum, merged by a tree at the end of a slice's piece;
+// Where the slices fit the CTAs well, every CTA's share lies in one slice: a share that straddles two
+// pays for their queries and their merge twice (about 4 us of 1.9 GHz).
+// Warps keep their own running maximum and sum, merged in a fixed order at the end of a slice's piece;
 // the last CTA to finish a slice (a ticket) merges the CTAs' states in order, so the result does
 // not depend on timing.
 //
@@ -208,14 +210,14 @@ struct Unit {
   long long off;   // block: byte offset in the pool; list: index of its first entry
   unsigned info;   // attended rows (16 bits), kList
   int s;           // slice
+  int bg;          // its sequence (<< 8) and head
 };
 // Listed rows on their way.
 struct Rows {
-  int pos, id, s;   // lane l < 16: position of row l (-1: not attended or not listed) and its page; the slice
+  int pos, id;      // lane l: position of row l of the item (-1: not attended or not listed) and its page
+  int s, bg;        // the slice, its sequence (<< 8) and head
 };
 constexpr unsigned kList = 0x10000u;
-
-constexpr int kMergeWords = 9 * 32 * 4;   // a warp's state as its lanes hold it: 32 sums, maximum and sum
 
 // Rotated queries in shared memory: the dims 32 apart of 8 heads fall into 32 banks.
 constexpr int kQRow = 161;
@@ -232,15 +234,15 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* const ring = smem;                                              // [W][S][U][kBlk]
   float* const mbuf = reinterpret_cast<float*>(smem + (size_t)W * S * U * kBlk);     // [(W + 1) / 2][kMergeWords]
-  float* const cbuf = mbuf + (W + 1) / 2 * kMergeWords;              // [max(W, 8)][kPartStride]
-  float* const qs = cbuf + (W > kMaxGroup ? W : kMaxGroup) * kPartStride;        // [8][kQRow]
+  float* const qs = mbuf + (W + 1) / 2 * kMergeWords;                            // [8][kQRow]
   long long* const rpre = reinterpret_cast<long long*>(qs + kMaxGroup * kQRow);  // [n_slices + 1]
   int2* const sinfo = reinterpret_cast<int2*>(rpre + A.n_slices + 1);            // [n_slices] (L, listed rows)
   __shared__ __align__(8) unsigned long long full[W * S];
   __shared__ unsigned vmask[W * S * U];   // attended rows of a slot's units; bit 16: gathered
   __shared__ long long shl[W];
   __shared__ int s_merge;
-  __shared__ float qtop[kMaxGroup];
+  __shared__ float qun[kMaxGroup];             // 4 bits: what a head's scores are multiplied by
+  __shared__ int4 s_split;                     // aligned shares: slice, its first CTA, its CTAs, -1: equal shares
   __shared__ uint4 qf[kF16 ? 8 * 32 : 1];      // 4 bits: query operands, a lane's 16 bytes of each k-step
   __shared__ float2 q8[kF16 ? 4 * 8 : 1];      // 4 bits: -8 times a scale group's sum of queries (high, residual), each head
   __shared__ __align__(16) float kscale[kF16 ? 4 * W * 32 : 4];   // 4 bits, of the item in hand: scales of K, by group and row
@@ -251,10 +253,14 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   const int NS = A.n_slices, Hkv = A.pool.Hkv, G = A.G;
 
   if (tid < W * S) mbar_init(smem_u32(&full[tid]), U);
+  if (kF16) {   // heads that the group does not have
+    if (tid < 256) qf[kF16 ? tid : 0] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 32) q8[kF16 ? tid : 0] = make_float2(0.f, 0.f);
+  }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
   // ---- item prefix over slices
-  bool whole;
+  bool small;   // no slice has more than two items a warp
   {
     long long carry = 0;
     bool big = false;
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       __syncthreads();
     }
     if (tid == 0) rpre[NS] = carry;
-    whole = !__syncthreads_or(big) && NS <= (int)gridDim.x;
+    small = !__syncthreads_or(big) && NS <= (int)gridDim.x;
   }
   const long long T = rpre[NS];
   // slices without a row: zeros
@@ -310,14 +316,77 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     for (int i = tid; i < G * kHeadDim; i += W * 32) A.out[h0 * kHeadDim + i] = 0.f;
     if (A.lse && tid < G) A.lse[h0 + tid] = -INFINITY;
   }
-  // Equal shares, down to one item a CTA.  Where there are CTAs enough and no slice has more than two items a
-  // warp, a CTA takes one slice: nothing is left to merge between CTAs.
-  long long r_lo, r_hi;
+  // ---- shares.  A CTA a slice where those are small and few.  Else aligned to slices: a slice of n items takes
+  // ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice; taken where its
+  // largest share is within kPieceItems of the equal share: what a second slice would cost a CTA.  Else
+  // equal shares, down to one item a CTA.
+  constexpr int kLaneSlices = 5, kPieceItems = 12;
+  if (!small) {
+    if (NS > 32 * kLaneSlices || NS > (int)gridDim.x) {
+      if (tid == 0) s_split = make_int4(0, 0, -1, 0);
+    } else if (warp == 0) {
+      float n[kLaneSlices];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kLaneSlices; ++i) {
+        const int s = lane * kLaneSlices + i;
+        n[i] = s < NS ? (float)(rpre[s + 1] - rpre[s]) : 0.f;
+        top = fmaxf(top, n[i]);
+      }
+      top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+      const float equal = __fdividef((float)T, (float)gridDim.x);
+      float most = fmaxf(equal, (float)W);
+      int k[kLaneSlices], sum = 0;
+#pragma unroll 1
+      for (int t = 0; t < 9; ++t) {
+        const float inv = __fdividef(0.999999f, most);
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneSlices; ++i) {
+          k[i] = (int)ceilf(n[i] * inv);
+          mine += k[i];
+        }
+        sum = __reduce_add_sync(kFull, mine);
+        if (sum <= (int)gridDim.x) break;
+        most = t == 7 ? top * 1.0001f : fmaxf(most * __fdividef((float)sum, (float)gridDim.x), most * 1.01f);
+      }
+      float share = 0.f;
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < kLaneSlices; ++i) {
+        if (k[i] > 0) share = fmaxf(share, __fdividef(n[i], (float)k[i]));
+        mine += k[i];
+      }
+      share = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(share)));
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= mine;
+      const bool fits = sum <= (int)gridDim.x && share <= equal + kPieceItems;
+      if (lane == 0) s_split = make_int4(0, 0, fits ? 0 : -1, 0);
+      __syncwarp();
+      if (fits) {
+#pragma unroll
+        for (int i = 0; i < kLaneSlices; ++i) {
+          if ((int)blockIdx.x >= before && (int)blockIdx.x < before + k[i]) s_split = make_int4(lane * kLaneSlices + i, before, k[i], 0);
+          before += k[i];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int4 split = small ? make_int4(blockIdx.x, blockIdx.x, (int)blockIdx.x < NS ? 1 : 0, 0) : s_split;
+  const bool aligned = split.z >= 0;
   const int nb = (long long)gridDim.x < T ? (int)gridDim.x : (int)T;
-  if (whole) {
-    if ((int)blockIdx.x >= NS) return;
-    r_lo = rpre[blockIdx.x];
-    r_hi = rpre[blockIdx.x + 1];
+  long long r_lo, r_hi;
+  if (aligned) {
+    if (split.z == 0) return;
+    const long long n = rpre[split.x + 1] - rpre[split.x];
+    r_lo = rpre[split.x] + (blockIdx.x - split.y) * n / split.z;
+    r_hi = rpre[split.x] + (blockIdx.x - split.y + 1) * n / split.z;
     if (r_lo == r_hi) return;
   } else {
     if ((int)blockIdx.x >= nb) return;
@@ -334,25 +403,52 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     }
     return lo;
   };
-  const int s_first = slice_of(r_lo), s_last = slice_of(r_hi - 1);
+  const int s_first = aligned ? split.x : slice_of(r_lo), s_last = aligned ? split.x : slice_of(r_hi - 1);
+
+  // ---- a slice's queries: warp h takes head h of the group, a lane the pairs lane and lane + 32
+  const int half = tab.rot / 2;
+  auto pair_at = [&](int j, int& d0, int& d1) {
+    d0 = j >= half ? tab.rot + 2 * (j - half) : tab.interleaved ? 2 * j : j;
+    d1 = j >= half || tab.interleaved ? d0 + 1 : d0 + half;
+  };
+  auto load_q = [&](int s) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp < G) {
+      const size_t at = ((size_t)(s / Hkv) * A.Hq + (size_t)(s % Hkv) * G + warp) * kHeadDim;
+      int a0, a1, b0, b1;
+      pair_at(lane, a0, a1);
+      pair_at(lane + 32, b0, b1);
+      if (A.q_f32) {
+        const float* q = static_cast<const float*>(A.q) + at;
+        x = make_float4(q[a0], q[a1], q[b0], q[b1]);
+      } else {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + at;
+        x = make_float4(__bfloat162float(q[a0]), __bfloat162float(q[a1]), __bfloat162float(q[b0]), __bfloat162float(q[b1]));
+      }
+    }
+    return x;
+  };
+  float4 q_next = load_q(s_first);
   const uint32_t ring_a = smem_u32(ring) + warp * S * U * kBlk, bar_a = smem_u32(&full[warp * S]);
   const uint64_t pol = l2_evict_first();
 
   // ---- the warp's items r_lo + warp + W k, k < nk: lane i looks up unit i % U of item kItems j + i / U
   const int nk = r_lo + warp < r_hi ? (int)((r_hi - r_lo - warp + W - 1) / W) : 0;
+  auto page_of = [&](unsigned blk) { return A.pool.page_blocks == 1 ? blk : __umulhi(blk, A.by_blocks); };
   auto find = [&](int k) {
     Unit X;
-    X.s = 0;
+    X.s = X.bg = 0;
     X.off = 0;
     X.info = 0u;
     k += lane / U;
     if (k >= nk) return X;
     const long long r = r_lo + warp + (long long)W * k;
     const int s = slice_of(r);
-    const int b = s / Hkv, g = s - b * Hkv;
+    const int b = Hkv == 1 ? s : (int)__umulhi((unsigned)s, A.by_heads), g = s - b * Hkv;
     const Slice sl = make_slice(A, g, sinfo[s].x, sinfo[s].y);
     const int u = (int)(r - rpre[s]) * U + lane % U;
     X.s = s;
+    X.bg = b << 8 | g;
     if (u >= units_of(sl)) return X;
     if (LISTED && u >= sl.nb0 + sl.nb1) {
       const int i = (u - sl.nb0 - sl.nb1) * 16;
@@ -365,7 +461,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     // rows [0, L), below n_s or at least w_lo
     auto below = [&](int q) { return q <= p0 ? 0u : 0xffffu >> (16 - min(16, q - p0)); };
     const unsigned rows = below(sl.L) & (below(sl.n_s) | ~below(sl.w_lo));
-    const unsigned pg = (unsigned)blk / (unsigned)A.pool.page_blocks, in = (unsigned)blk - pg * (unsigned)A.pool.page_blocks;
+    const unsigned pg = page_of((unsigned)blk), in = (unsigned)blk - pg * (unsigned)A.pool.page_blocks;
     const int id = __ldg(A.pool.table + (size_t)b * A.pool.max_pages + pg);
     if ((unsigned)id < (unsigned)A.pool.n_pages) {
       X.off = ((long long)id * Hkv + g) * A.pool.head_bytes + (long long)in * kBlk;
@@ -381,7 +477,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   auto list_rows = [&](int k) {   // starts the loads of item k's positions
     Rows R;
     R.pos = R.id = -1;
-    R.s = 0;
+    R.s = R.bg = 0;
     if (k >= nk) return R;
     const Unit& B = k / kItems == ki / kItems ? cur : nxt;
     const int from = k % kItems * U + (U == 2 ? lane >> 4 : 0);
@@ -389,6 +485,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     if (!__any_sync(kFull, info & kList)) return R;
     const long long off = __shfl_sync(kFull, B.off, from);
     R.s = __shfl_sync(kFull, B.s, from);
+    R.bg = __shfl_sync(kFull, B.bg, from);
     if (lane < 16 * U && (info & kList) && (info >> (lane & 15) & 1u)) {
       R.pos = __ldg(A.list + off + (lane & 15));
       if (R.pos < 0) R.pos = INT_MAX;   // refused with the positions past the end
@@ -402,8 +499,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       R.pos = -1;
       return;
     }
-    const unsigned pg = ((unsigned)R.pos / kBlockTok) / (unsigned)A.pool.page_blocks;
-    R.id = __ldg(A.pool.table + (size_t)(R.s / Hkv) * A.pool.max_pages + pg);
+    R.id = __ldg(A.pool.table + (size_t)(R.bg >> 8) * A.pool.max_pages + page_of((unsigned)R.pos / kBlockTok));
   };
   Rows r0, r1;   // of items ki and ki + 1
   if (LISTED) {
@@ -434,36 +530,32 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         const bool page_ok = (unsigned)r0.id < (unsigned)A.pool.n_pages;
         if (r0.pos >= 0 && !page_ok) atomicOr(A.pool.err, kErrPage);
         const unsigned m = __ballot_sync(kFull, r0.pos >= 0 && page_ok);
-        const unsigned in = ((unsigned)r0.pos / kBlockTok) % (unsigned)A.pool.page_blocks;
-        // block offset (a multiple of 256) and row
-        const long long from = page_ok ? ((long long)r0.id * Hkv + r0.s % Hkv) * A.pool.head_bytes + (long long)in * kBlk +
-                                             (r0.pos & (kBlockTok - 1)) : 0;
+        // row of the pool, in rows of a head: memory holds fewer than 2^32
+        const unsigned blkno = (unsigned)r0.pos / kBlockTok, in = blkno - page_of(blkno) * (unsigned)A.pool.page_blocks;
+        const unsigned from = (((unsigned)r0.id * Hkv + (r0.bg & 255)) * A.pool.page_blocks + in) * kBlockTok + (r0.pos & (kBlockTok - 1));
         if (FMT == kPageInt4) {
 #pragma unroll
           for (int i = 0; i < 2 * U; ++i) {
             const int r = i * 8 + gid;   // row of the item
-            const long long a = __shfl_sync(kFull, from, r);
+            const unsigned a = __shfl_sync(kFull, from, r);
             if (m >> r & 1u) {
-              const int rin = (int)(a & 15);
-              const unsigned char* src = A.pool.pages + (a - rin) + rin * kRow4 + t4 * 16;
+              const unsigned char* src = A.pool.pages + (size_t)(a / kBlockTok) * kBlk + (a % kBlockTok) * kRow4 + t4 * 16;
               const uint32_t d = dst + i / 2 * kBlk + (r & 15) * kRow4 + t4 * 16;
               cp_async16(d, src);
               cp_async16(d + kBlockTok * kRow4, src + kBlockTok * kRow4);
             }
           }
           if (m >> lane & 1u) {
-            const int rin = (int)(from & 15);
             cp_async16(dst + lane / 16 * kBlk + 2 * kBlockTok * kRow4 + (lane & 15) * 16,
-                       A.pool.pages + (from - rin) + 2 * kBlockTok * kRow4 + rin * 16);
+                       A.pool.pages + (size_t)(from / kBlockTok) * kBlk + 2 * kBlockTok * kRow4 + (from % kBlockTok) * 16);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = i * 2 + (lane >> 4), c = lane & 15;
-            const long long a = __shfl_sync(kFull, from, r);
+            const unsigned a = __shfl_sync(kFull, from, r), rin = a % kBlockTok;
             if (m >> r & 1u) {
-              const int rin = (int)(a & 15);
-              const unsigned char* src = A.pool.pages + (a - rin) + rin * 256 + ((c ^ (rin & 7)) << 4);
+              const unsigned char* src = A.pool.pages + (size_t)(a / kBlockTok) * kBlk + rin * 256 + ((c ^ (rin & 7)) << 4);
               const uint32_t d = dst + r * 256 + ((c ^ (r & 7)) << 4);
               cp_async16(d, src);
               cp_async16(d + kBlockTok * 256, src + kBlockTok * 256);
@@ -503,75 +595,62 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     const int b = s / Hkv, g = s - b * Hkv;
     const size_t h0 = (size_t)b * A.Hq + (size_t)g * G;
     // ---- the group's queries, rotated at position L - 1, times scale / ln 2
-    {
-      const int pos = sinfo[s].x - 1, half = tab.rot / 2;
-      for (int x = tid; x < G * (kHeadDim / 2); x += W * 32) {
-        const int h = x >> 6, j = x & 63;
-        const int d0 = j >= half ? tab.rot + 2 * (j - half) : tab.interleaved ? 2 * j : j;
-        const int d1 = j >= half || tab.interleaved ? d0 + 1 : d0 + half;
-        float q0, q1;
-        if (A.q_f32) {
-          const float* q = static_cast<const float*>(A.q) + (h0 + h) * kHeadDim;
-          q0 = q[d0];
-          q1 = q[d1];
-        } else {
-          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + (h0 + h) * kHeadDim;
-          q0 = __bfloat162float(q[d0]);
-          q1 = __bfloat162float(q[d1]);
-        }
+    if (warp < G) {
+      float* const q = qs + warp * kQRow;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = lane + 32 * i;
+        int d0, d1;
+        pair_at(j, d0, d1);
+        const float q0 = i ? q_next.z : q_next.x, q1 = i ? q_next.w : q_next.y;
         float c = 1.f, sn = 0.f;
-        if (j < half) rope_cs(tab.f_pi[j], (double)pos, (float)tab.mag, c, sn);
-        qs[h * kQRow + q_at(d0)] = (q0 * c - q1 * sn) * A.scale_log2;
-        qs[h * kQRow + q_at(d1)] = (q0 * sn + q1 * c) * A.scale_log2;
+        if (j < half) rope_cs(tab.f_pi[j], (double)(sinfo[s].x - 1), (float)tab.mag, c, sn);
+        q[q_at(d0)] = (q0 * c - q1 * sn) * A.scale_log2;
+        q[q_at(d1)] = (q0 * sn + q1 * c) * A.scale_log2;
       }
-      __syncthreads();
+      if (kF16) {
+        __syncwarp();
+        // dim lane + 32 t of scale group lane / 8: k-step 2 (lane / 8) + i holds dims 32 t + 8 (lane / 8) + 2 i + {0, 4, 1, 5}
+        float x[4], top = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          x[t] = q[q_at(lane + 32 * t)];
+          top = fmaxf(top, fabsf(x[t]));
+        }
+        top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
+        const bool odd = lane & 1;   // the operand's second half, whose codes count 16 times
+        const float f = __uint_as_float((unsigned)(127 + 10 - e) << 23) * (odd ? 0.0625f : 1.f);
+        if (lane == 0) qun[warp] = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kCodeUnit;
+        const int kk = 2 * (lane >> 3) + ((lane & 3) >> 1);
+        float sh = 0.f, sl = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const __half hi = __float2half_rn(x[t] * f), lo = __float2half_rn(x[t] * f - __half2float(hi));
+          __half* const to = reinterpret_cast<__half*>(qf + 32 * kk + 4 * warp + t) + (odd ? 4 : 0) + ((lane >> 2) & 1);
+          to[0] = hi;
+          to[2] = lo;
+          sh += __half2float(hi);
+          sl += __half2float(lo);
+        }
+        if (odd) {
+          sh *= 16.f;
+          sl *= 16.f;
+        }
+#pragma unroll
+        for (int o = 1; o <= 4; o <<= 1) {
+          sh += __shfl_xor_sync(kFull, sh, o);
+          sl += __shfl_xor_sync(kFull, sl, o);
+        }
+        if ((lane & 7) == 0) q8[8 * (lane >> 3) + warp] = make_float2(sh * (-8.f / kCodeUnit), sl * (-8.f / kCodeUnit));
+      }
     }
-    // A operand: 4 bits: k-step 2w + i of word w holds dims 32 t4 + 8 w + 2 i + {0, 4, 1, 5}, in shared
-    // memory; bf16: natural order, in registers
+    __syncthreads();
+    // A operand: 4 bits in shared memory, bf16 in registers and in natural order
     uint32_t qa[kF16 ? 1 : 8][4];
     uint32_t qb[WIDE ? 8 : 1][2];   // the low part's rows where they need a product of their own
-    float unscale = 1.f;
-    if (kF16) {
-      for (int h = warp; h < G; h += W) {   // the heads' largest components
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(qs[h * kQRow + q_at(lane + 32 * k)]));
-        top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
-        if (lane == 0) qtop[h] = top;
-      }
-      __syncthreads();
-      const float top = qtop[gid < G ? gid : 0];
-      const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
-      const float f = gid < G ? __uint_as_float((unsigned)(127 + 10 - e) << 23) : 0.f;
-      unscale = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kCodeUnit;
-      const float* q = qs + (gid < G ? gid : 0) * kQRow + q_at(32 * t4);
-      for (int kk = warp; kk < 8; kk += W) {
-        const float* x = q + 8 * (kk >> 1) + 2 * (kk & 1);
-        __half2 h[2], lo[2];
-        split_f16(x[0] * f, x[4] * f, h[0], lo[0]);
-        split_f16(x[1] * (f * 0.0625f), x[5] * (f * 0.0625f), h[1], lo[1]);
-        qf[32 * kk + lane] = make_uint4(bits(h[0]), bits(lo[0]), bits(h[1]), bits(lo[1]));
-      }
-      __syncthreads();
-      if (warp < 4) {
-        float2 t = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const uint4 v = qf[32 * (2 * warp + kk) + lane];
-          const float2 h0_ = __half22float2(half2_of(v.x)), l0 = __half22float2(half2_of(v.y));
-          const float2 h1 = __half22float2(half2_of(v.z)), l1 = __half22float2(half2_of(v.w));
-          t.x += (h0_.x + h0_.y) + 16.f * (h1.x + h1.y);
-          t.y += (l0.x + l0.y) + 16.f * (l1.x + l1.y);
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          t.x += __shfl_xor_sync(kFull, t.x, o);
-          t.y += __shfl_xor_sync(kFull, t.y, o);
-        }
-        if (t4 == 0) q8[8 * warp + gid] = make_float2(t.x * (-8.f / kCodeUnit), t.y * (-8.f / kCodeUnit));
-      }
-      __syncthreads();
-    } else {
+    const float unscale = kF16 ? qun[gid < G ? gid : 0] : 1.f;
+    if (!kF16) {
       const int h = WIDE ? gid : gid & 3;
       const bool in = h < G;
 #pragma unroll
@@ -838,33 +917,24 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         else if (!WIDE) o[nt][e] += __shfl_xor_sync(kFull, o[nt][e], 16);
       }
     }
-    // dims of (column tile nt, e): 4 bits 32 t4 + 16 e + nt, bf16 8 nt + 2 t4 + e
-    auto put = [&](float* dst) {
+    // ---- the warps' states as their lanes hold them: the upper half of the warps hands over to the lower, then thread x
+    // takes 4 of the 32 sums of one lane over what is left
+    constexpr int kBoxes = (W + 1) / 2;
+    float4* const box = reinterpret_cast<float4*>(mbuf + (size_t)(warp % kBoxes) * kMergeWords) + lane;
+    auto hand_over = [&]() {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int nt = 0; nt < 16; nt += 4)
-          if (FMT == kPageInt4)
-            *reinterpret_cast<float4*>(dst + 32 * t4 + 16 * e + nt) = make_float4(o[nt][e], o[nt + 1][e], o[nt + 2][e], o[nt + 3][e]);
-          else if (e == 0)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<float2*>(dst + 8 * (nt + k) + 2 * t4) = make_float2(o[nt + k][0], o[nt + k][1]);
+      for (int k = 0; k < 8; ++k) box[32 * k] = make_float4(o[2 * k][0], o[2 * k][1], o[2 * k + 1][0], o[2 * k + 1][1]);
+      box[256] = make_float4(m, l, 0.f, 0.f);
     };
-#pragma unroll 1
-    for (int n = W; n > 1; n = (n + 1) / 2) {
-      const int half = (n + 1) / 2;   // warps half .. n - 1 hand over to 0 ..
-      float4* const box = reinterpret_cast<float4*>(mbuf + (size_t)(warp >= half ? warp - half : warp) * kMergeWords) + lane;
-      if (warp >= half && warp < n) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) box[32 * k] = make_float4(o[2 * k][0], o[2 * k][1], o[2 * k + 1][0], o[2 * k + 1][1]);
-        box[256] = make_float4(m, l, 0.f, 0.f);
-      }
-      __syncthreads();
-      if (warp < n - half) {
+    if (warp >= kBoxes) hand_over();
+    int s_after = s + 1;
+    while (s_after <= s_last && rpre[s_after + 1] == rpre[s_after]) ++s_after;
+    if (s_after <= s_last) q_next = load_q(s_after);
+    __syncthreads();
+    if (warp < kBoxes) {
+      if (warp + kBoxes < W) {
         const float4 ml = box[256];
-        const float mn = fmaxf(m, ml.x);
-        const float sa = exp2f(m - mn), sb = exp2f(ml.x - mn);
+        const float mn = fmaxf(m, ml.x), sa = exp2f(m - mn), sb = exp2f(ml.x - mn);
         l = l * sa + ml.y * sb;
         m = mn;
 #pragma unroll
@@ -876,111 +946,100 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
           o[2 * k + 1][1] = o[2 * k + 1][1] * sa + v.w * sb;
         }
       }
-      __syncthreads();
+      hand_over();
     }
-    // ---- alone on the slice: the output; else its state, and the last CTA merges them
-    const int c0 = whole ? 0 : owner(rpre[s]), c1 = whole ? 0 : owner(rpre[s + 1] - 1);
-    if (warp == 0 && gid < G) {
-      float* dst;
-      if (c0 == c1) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;   // no weight at all: zeros
-#pragma unroll
-        for (int nt = 0; nt < 16; ++nt) {
-          o[nt][0] *= inv;
-          o[nt][1] *= inv;
-        }
-        dst = A.out + (h0 + gid) * kHeadDim;
-        if (A.lse && t4 == 0) A.lse[h0 + gid] = l == 0.f ? -INFINITY : m + log2f(l);
+    __syncthreads();
+    const int c0 = aligned ? split.y : owner(rpre[s]), c1 = aligned ? split.y + split.z - 1 : owner(rpre[s + 1] - 1);
+    const int xl = tid & 31, xh = xl >> 2;   // thread x: lane xl's sums of column tiles 2 (x / 32) and the next; its head
+    const bool takes = tid < 256 && xh < G;
+    float4* const part = reinterpret_cast<float4*>(A.part);
+    constexpr int kState = kMergeWords / 4;
+    // normalised sums of 4, to the output
+    auto put = [&](float4 v, float M, float Ls) {
+      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;   // no weight at all: zeros
+      const int k2 = 2 * (tid >> 5);                  // column tile
+      float* const to = A.out + (h0 + xh) * kHeadDim;
+      // (tile nt, e) is dim 32 t4 + 16 e + nt in 4 bits, 8 nt + 2 t4 + e in bf16
+      if (kF16) {
+        float2* const at = reinterpret_cast<float2*>(to + 32 * (xl & 3) + k2);
+        at[0] = make_float2(v.x * inv, v.z * inv);
+        at[8] = make_float2(v.y * inv, v.w * inv);
       } else {
-        dst = A.part + ((size_t)(blockIdx.x + s) * G + gid) * kPartStride;
-        if (t4 == 0) {
-          dst[kHeadDim] = m;
-          dst[kHeadDim + 1] = l;
-        }
+        float2* const at = reinterpret_cast<float2*>(to + 8 * k2 + 2 * (xl & 3));
+        at[0] = make_float2(v.x * inv, v.y * inv);
+        at[4] = make_float2(v.z * inv, v.w * inv);
       }
-      put(dst);
-      __threadfence();
+      if (A.lse && tid < 32 && (xl & 3) == 0) A.lse[h0 + xh] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
+    };
+    if (takes) {
+      float M = kNoMax, Ls = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      float2 ml[kBoxes];
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) {
+        ml[i] = *reinterpret_cast<const float2*>(mbuf + (size_t)i * kMergeWords + 1024 + 4 * xl);
+        M = fmaxf(M, ml[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) {
+        const float w = exp2f(ml[i].x - M);
+        const float4 v = *reinterpret_cast<const float4*>(mbuf + (size_t)i * kMergeWords + 4 * tid);
+        Ls += ml[i].y * w;
+        num.x += v.x * w;
+        num.y += v.y * w;
+        num.z += v.z * w;
+        num.w += v.w * w;
+      }
+      if (c0 == c1) {
+        put(num, M, Ls);
+      } else {
+        float4* const to = part + (size_t)(blockIdx.x + s) * kState;
+        to[tid] = num;
+        if (tid < 32) to[256 + xl] = make_float4(M, Ls, 0.f, 0.f);
+        __threadfence();
+      }
     }
     if (c0 == c1) continue;
+    // ---- the last CTA of the slice merges the CTAs' states in order
     __syncthreads();
     if (tid == 0) s_merge = atomicAdd(&A.ticket[s], 1u) == (unsigned)(c1 - c0);
     __syncthreads();
     if (!s_merge) continue;
     __threadfence();
-    // part x of G per: head x % G, states c0 + x / G, c0 + x / G + per, ...; then the parts of a head in order
-    {
-      const int per = max(1, W / G);
-      for (int x = warp; x < G * per; x += W) {
-        const int h = x % G, sub = x / G;
-        float M = kNoMax, Ls = 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kB = 8;
-        for (int c = c0 + sub; c <= c1; c += per * kB) {
-          float4 v[kB];
-          float mi[kB], li[kB];
+    if (takes) {
+      float M = kNoMax, Ls = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int kB = 8;
+      for (int c = c0; c <= c1; c += kB) {
+        float4 v[kB], ml[kB];
 #pragma unroll
-          for (int i = 0; i < kB; ++i) {
-            const int cc = c + i * per;
-            mi[i] = kNoMax;
-            li[i] = 0.f;
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (cc <= c1) {
-              const float* src = A.part + ((size_t)(cc + s) * G + h) * kPartStride;
-              v[i] = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-              mi[i] = __ldcg(src + kHeadDim);
-              li[i] = __ldcg(src + kHeadDim + 1);
-            }
-          }
+        for (int i = 0; i < kB; ++i) {
+          const float4* from = part + (size_t)(min(c + i, c1) + s) * kState;
+          v[i] = __ldcg(from + tid);
+          ml[i] = __ldcg(from + 256 + xl);
+        }
 #pragma unroll
-          for (int i = 0; i < kB; ++i) {
-            const float mn = fmaxf(M, mi[i]);
-            const float sa = exp2f(M - mn), sb = exp2f(mi[i] - mn);
-            Ls = Ls * sa + li[i] * sb;
-            num.x = num.x * sa + v[i].x * sb;
-            num.y = num.y * sa + v[i].y * sb;
-            num.z = num.z * sa + v[i].z * sb;
-            num.w = num.w * sa + v[i].w * sb;
-            M = mn;
-          }
-        }
-        float* mine = cbuf + (size_t)x * kPartStride;
-        *reinterpret_cast<float4*>(mine + 4 * lane) = num;
-        if (lane == 0) {
-          mine[kHeadDim] = M;
-          mine[kHeadDim + 1] = Ls;
-        }
-      }
-      __syncthreads();
-      for (int h = warp; h < G; h += W) {
-        float M = kNoMax, Ls = 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < per; ++k) {
-          const float* src = cbuf + (size_t)(h + G * k) * kPartStride;
-          const float m2 = src[kHeadDim], l2 = src[kHeadDim + 1];
-          const float mn = fmaxf(M, m2);
-          const float sa = exp2f(M - mn), sb = exp2f(m2 - mn);
-          const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
-          Ls = Ls * sa + l2 * sb;
-          num.x = num.x * sa + v.x * sb;
-          num.y = num.y * sa + v.y * sb;
-          num.z = num.z * sa + v.z * sb;
-          num.w = num.w * sa + v.w * sb;
+        for (int i = 0; i < kB; ++i) {
+          if (c + i > c1) break;
+          const float mn = fmaxf(M, ml[i].x), sa = exp2f(M - mn), sb = exp2f(ml[i].x - mn);
+          Ls = Ls * sa + ml[i].y * sb;
+          num.x = num.x * sa + v[i].x * sb;
+          num.y = num.y * sa + v[i].y * sb;
+          num.z = num.z * sa + v[i].z * sb;
+          num.w = num.w * sa + v[i].w * sb;
           M = mn;
         }
-        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
-        reinterpret_cast<float4*>(A.out + (h0 + h) * kHeadDim)[lane] = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-        if (A.lse && lane == 0) A.lse[h0 + h] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
       }
-      if (tid == 0) A.ticket[s] = 0u;   // ready for the next call
-      __syncthreads();
+      put(num, M, Ls);
     }
+    if (tid == 0) A.ticket[s] = 0u;   // ready for the next call
   }
 }
 
 template <int FMT, int W, int U, int S>
 constexpr size_t smem_bytes(int n_slices) {
   const size_t blk = FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
-  return W * U * S * blk + (size_t)((W + 1) / 2 * kMergeWords + (W > kMaxGroup ? W : kMaxGroup) * kPartStride) * 4 + kMaxGroup * kQRow * 4 +
+  return W * U * S * blk + (size_t)(W + 1) / 2 * kMergeWords * 4 + kMaxGroup * kQRow * 4 +
          (size_t)(n_slices + 1) * 8 + (size_t)n_slices * 8;
 }
 constexpr size_t smem_most(int format) { return (format == kPageInt4 ? 212 : 226) * 1024; }   // 227 KB less the static arrays

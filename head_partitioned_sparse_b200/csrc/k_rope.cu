@@ -102,8 +102,8 @@ struct RopeArgs {
 // One item = (token, head group, chunk).  V elements of each half (half layout) or V
 // consecutive elements = V / 2 pairs (interleaved); V = 1 serves pairs of any alignment
 // (an interleaved pair is then two single loads).
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(256) k_rope(const RopeArgs a, const __grid_constant__ RopeTabAny tab) {
+template <typename T, int V, bool INTER, int N>
+__global__ void __launch_bounds__(256) k_rope(const RopeArgs a, const __grid_constant__ RopeTab<N> tab) {
   constexpr int kPairs = INTER ? (V + 1) / 2 : V;   // pairs of a chunk
   const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (item >= a.items) return;
@@ -199,6 +199,13 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a, const __grid_con
   }
 }
 
+template <typename T, int V, int N>
+cudaError_t go_tab(const RopeArgs& a, unsigned blocks, const RopeTab<N>& tab, cudaStream_t st) {
+  if (tab.interleaved) k_rope<T, V, true, N><<<blocks, 256, 0, st>>>(a, tab);
+  else k_rope<T, V, false, N><<<blocks, 256, 0, st>>>(a, tab);
+  return cudaGetLastError();
+}
+
 template <typename T, int V>
 cudaError_t go(RopeArgs a, int B, const RopeTabAny& tab, cudaStream_t st) {
   const bool inter = tab.interleaved != 0;
@@ -208,9 +215,14 @@ cudaError_t go(RopeArgs a, int B, const RopeTabAny& tab, cudaStream_t st) {
   a.items = (int64_t)B * a.T * a.head_groups * (a.n_rot + a.n_copy);
   const int64_t blocks = (a.items + 255) / 256;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  if (inter) k_rope<T, V, true><<<(unsigned)blocks, 256, 0, st>>>(a, tab);
-  else k_rope<T, V, false><<<(unsigned)blocks, 256, 0, st>>>(a, tab);
-  return cudaGetLastError();
+  // the table travels with the launch: a long one costs a decode step's call 4 us of the host's time
+  if (tab.rot > kHeadDim) return go_tab<T, V>(a, (unsigned)blocks, tab, st);
+  RopeTab128 t;
+  t.rot = tab.rot;
+  t.interleaved = tab.interleaved;
+  t.mag = tab.mag;
+  for (int i = 0; i < kHeadDim / 2; ++i) t.f_pi[i] = tab.f_pi[i];
+  return go_tab<T, V>(a, (unsigned)blocks, t, st);
 }
 
 }  // namespace

@@ -114,7 +114,7 @@ PagedPlan plan(const spa_paged_config& c, int grid) {
   const size_t slices = (size_t)c.max_batch * c.n_kv_heads;
   PagedPlan p;
   p.part = 0;
-  p.ticket = (grid + slices) * (c.n_q_heads / c.n_kv_heads) * spa::kPartStride * 4;
+  p.ticket = (grid + slices) * spa::kMergeWords * 4;
   p.err = (p.ticket + slices * 4 + 255) / 256 * 256;
   p.total = p.err + 256;
   return p;
@@ -406,6 +406,8 @@ spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, 
   a.q_f32 = h->cfg.kv_dtype == SPA_F32;
   a.n_sink = n_sink;
   a.window = window;
+  a.by_heads = (unsigned)(((1ull << 32) + h->cfg.n_kv_heads - 1) / h->cfg.n_kv_heads);
+  a.by_blocks = (unsigned)(((1ull << 32) + a.pool.page_blocks - 1) / a.pool.page_blocks);
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
   for (int g = 0; g < h->cfg.n_kv_heads; ++g) {
     const bool ret = !head_mask_opt || head_mask_opt[g];

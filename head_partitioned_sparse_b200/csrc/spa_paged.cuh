@@ -13,6 +13,7 @@ constexpr int kBlockBytes4 = 2 * kBlockTok * kRow4 + kBlockTok * 16;   // codes 
 constexpr int kBlockBytes16 = 2 * kBlockTok * kHeadDim * 2;
 constexpr int kMaxPagedSlices = 4096;               // max_batch * n_kv_heads (row prefix of the attention in shared memory)
 constexpr int kMaxRopePairs = 256;
+constexpr int kMergeWords = 9 * 32 * 4;             // a warp's or CTA's attention state as lanes hold it: 32 sums, maximum and sum
 
 // Device status bits of a paged cache (kErrSeqLen, kErrStartPos and kErrTimeout as for spa_handle).
 constexpr unsigned kErrPage = 16u;    // block_table entry outside [0, n_pages)
@@ -90,13 +91,15 @@ struct PagedAttendArgs {
   int64_t list_stride;
   float* out;              // [B][Hq][128]
   float* lse;              // optional [B][Hq]
-  float* part;             // [grid + n_slices][G][kPartStride]
+  float* part;             // [grid + n_slices][kMergeWords]
   unsigned* ticket;        // [n_slices], zero between calls
   int B, Hq, G, n_slices;
   int64_t cap;             // largest accepted length
   int q_f32;
   int n_sink, window;
   float scale_log2;
+  unsigned by_heads;       // ceil(2^32 / Hkv), ceil(2^32 / page_blocks): the high word of a product divides
+  unsigned by_blocks;      // slices (below 2^12) and blocks (below 2^20) exactly; unused for a divisor of 1
   unsigned char all_rows[kMaxKvHeads];   // the head attends every row
   unsigned char has_list[kMaxKvHeads];   // the head attends its list too
 };
