@@ -518,10 +518,15 @@ def spa_paged_page_bytes(cfg: spa_paged_config) -> int:
 def spa_paged_create(cfg: spa_paged_config, rope=None) -> int:
     h = ctypes.c_void_p(None)
     _check(load().spa_paged_create(ctypes.byref(h), ctypes.byref(cfg), rope))
+    _kv_heads[h.value] = cfg.n_kv_heads
     return h.value
 
 
+_kv_heads = {}   # of the paged handles: the length of a head mask
+
+
 def spa_paged_destroy(h) -> None:
+    _kv_heads.pop(h, None)
     _check(load().spa_paged_destroy(h))
 
 
@@ -556,6 +561,8 @@ def spa_attend_paged(h, q_pre, pages, block_table, seq_lens, B: int, max_seq_len
                      stream=None) -> None:
     """head_mask: None (every head attends every row), or the host mask [Hkv] (bytes, list or tensor)."""
     mask = head_mask if head_mask is None or head_mask.__class__ is bytes else _host_u8(head_mask)
+    if mask is not None and len(mask) != _kv_heads.get(h, len(mask)):
+        raise ValueError(f"head_mask has {len(mask)} entries, the handle {_kv_heads[h]} KV heads")
     d = _device()
     st = (_lib or load()).spa_attend_paged(h, _dev(q_pre, d), _dev(pages, d), _dev(block_table, d), _dev(seq_lens, d),
                                            B, max_seq_len, mask, n_sink, window, _dev(sel_idx, d), _dev(sel_count, d),

@@ -373,8 +373,7 @@ __global__ void __launch_bounds__(256, 2) k_page_append(const PagePool P, const 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int j = i % kAngles;
-          y[0][i] = fmaf(x[0][i], c[j], -x[1][i] * sn[j]);
-          y[1][i] = fmaf(x[1][i], c[j], x[0][i] * sn[j]);
+          turn(x[0][i], x[1][i], c[j], sn[j], y[0][i], y[1][i]);
         }
         xtop = __float_as_uint(top0 + top1);
       } else if (PAIR == kInLane) {
@@ -386,8 +385,9 @@ __global__ void __launch_bounds__(256, 2) k_page_append(const PagePool P, const 
             // dims that do not turn stay out of it: their neighbours may be infinite
             const bool turns = 8 * R.e + 64 * h + 2 * i < tab.rot;
             const float u = x[h][2 * i], w = x[h][2 * i + 1];
-            y[h][2 * i] = turns ? fmaf(u, c[j], -w * sn[j]) : u;
-            y[h][2 * i + 1] = turns ? fmaf(w, c[j], u * sn[j]) : w;
+            y[h][2 * i] = u;
+            y[h][2 * i + 1] = w;
+            if (turns) turn(u, w, c[j], sn[j], y[h][2 * i], y[h][2 * i + 1]);
           }
         xtop = max(__float_as_uint(top0 + top0), __float_as_uint(top1 + top1));
       } else {

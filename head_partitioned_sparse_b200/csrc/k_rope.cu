@@ -176,16 +176,14 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a, const __grid_con
 #pragma unroll
             for (int i = 0; i < V; ++i) {
               const float u0 = f0[i], v0 = f1[i];
-              f0[i] = u0 * c[i] - v0 * s[i];
-              f1[i] = u0 * s[i] + v0 * c[i];
+              turn(u0, v0, c[i], s[i], f0[i], f1[i]);
             }
             p1[u].set(f1);
           } else {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
               const float u0 = f0[2 * i], v0 = f0[2 * i + 1];
-              f0[2 * i] = u0 * c[i] - v0 * s[i];
-              f0[2 * i + 1] = u0 * s[i] + v0 * c[i];
+              turn(u0, v0, c[i], s[i], f0[2 * i], f0[2 * i + 1]);
             }
           }
           p0[u].set(f0);

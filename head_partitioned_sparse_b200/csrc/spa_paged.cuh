@@ -46,6 +46,12 @@ __device__ __forceinline__ void rope_cs(double f_pi, double pos, float mag, floa
   s = sn * mag;
 }
 
+// A pair turned: the same roundings wherever rows are rotated.
+__device__ __forceinline__ void turn(float u, float v, float c, float s, float& a, float& b) {
+  a = fmaf(u, c, -(v * s));
+  b = fmaf(v, c, u * s);
+}
+
 // Strides of a [batch][token][head][128] tensor, in elements.
 struct Strides3 {
   int64_t b, t, h;
