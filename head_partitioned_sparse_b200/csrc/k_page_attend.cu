@@ -23,13 +23,12 @@
 //   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
 //     to a maximum of 2^10 a head; probabilities are 2^11 times their value and value scales at most 2^4
 //     by the largest scale the warp has met (a power of two, moved like the running maximum), so
-//     float16's range holds both.  A code word (8 nibbles) becomes four float16 pairs, (nibble j,
-//     nibble j + 4), by a mask each: small integers under a zero exponent are subnormals.
+//     float16's range holds both.  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
 //     are summed by themselves (starting at -8 times the sum of the queries, which centres
 //     the codes) and scaled once a (row, group), not once an element.
 //     Values: the halves of two rows' words are merged by one byte permute into (row, row + 1)
-//     pairs and centred by an addition (their sums run over the whole context: no cancellation is
+//     pairs and centred by a multiply-add (their sums run over the whole context: no cancellation is
 //     put into them); column tile t holds dims 16 n + t, all of scale group t / 4, whose
 //     scales go into the probabilities (four sets of them, in packed float16 with exact residuals).
 //   bf16: three bf16 parts (24 bits).  Up to 4 heads they share one operand (high rows 0-3, middle rows 4-7, low
@@ -107,11 +106,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // d = A B + c, c.x in the upper rows and c.y in the lower ones.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, float2 c) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%10,%11,%11};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y));
+template <bool F16>
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float2 c) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%11,%11};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%11,%11};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y));
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -138,23 +144,28 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w as float16 pairs of n 2^-24, the second and fourth 16 times that.
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w as float16 pairs of n 2^-22, the second and fourth 16 times that: a
+// mask each, since small integers under a zero exponent are subnormals.  The tensor cores align a product by its
+// operands' exponent fields, so a subnormal's leading zeros are lost from the sum: as high up as two
+// pairs of a shift can go they cost 2^-22 of the sum (at the bottom, 2^-20).
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t v = w >> 8;
-  r[0] = w & 0x000f000fu;
-  r[1] = w & 0x00f000f0u;
-  r[2] = v & 0x000f000fu;
-  r[3] = v & 0x00f000f0u;
+  const uint32_t u = w << 2, v = w >> 6;
+  r[0] = u & 0x003c003cu;
+  r[1] = u & 0x03c003c0u;
+  r[2] = v & 0x003c003cu;
+  r[3] = v & 0x03c003c0u;
 }
-// The same of n - 8 (exact).
+constexpr float kKeyUnit = 4194304.f;   // 2^22: what a key's code of 1 stands for, inverted
+// The same nibbles as (n - 8) 2^-10, normal numbers and exact.
 __device__ __forceinline__ void centred_pairs(uint32_t w, uint32_t (&r)[4]) {
-  code_pairs(w, r);
-  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[0]) : "r"(0x80088008u));
-  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[1]) : "r"(0x80808080u));
-  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[2]) : "r"(0x80088008u));
-  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[3]) : "r"(0x80808080u));
+  const uint32_t v = w >> 8;
+  const uint32_t up = 0x74007400u, up16 = 0x64006400u, centre = 0xa000a000u;   // 2^14, 2^10, -8 2^-10
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[0]) : "r"(w & 0x000f000fu), "r"(up), "r"(centre));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(w & 0x00f000f0u), "r"(up16), "r"(centre));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[2]) : "r"(v & 0x000f000fu), "r"(up), "r"(centre));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(v & 0x00f000f0u), "r"(up16), "r"(centre));
 }
-constexpr float kCodeUnit = 16777216.f;   // 2^24: what a code of 1 stands for in float16, inverted
+constexpr float kValueUnit = 1024.f;   // 2^10: what a value's code of 1 stands for, inverted
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 // Float16 high parts and residuals of a pair.
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
         const bool odd = lane & 1;   // the operand's second half, whose codes count 16 times
         const float f = __uint_as_float((unsigned)(127 + 10 - e) << 23) * (odd ? 0.0625f : 1.f);
-        if (lane == 0) qun[warp] = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kCodeUnit;
+        if (lane == 0) qun[warp] = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kKeyUnit;
         const int kk = 2 * (lane >> 3) + ((lane & 3) >> 1);
         float sh = 0.f, sl = 0.f;
 #pragma unroll
@@ -642,7 +653,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
           sh += __shfl_xor_sync(kFull, sh, o);
           sl += __shfl_xor_sync(kFull, sl, o);
         }
-        if ((lane & 7) == 0) q8[8 * (lane >> 3) + warp] = make_float2(sh * (-8.f / kCodeUnit), sl * (-8.f / kCodeUnit));
+        if ((lane & 7) == 0) q8[8 * (lane >> 3) + warp] = make_float2(sh * (-8.f / kKeyUnit), sl * (-8.f / kKeyUnit));
       }
     }
     __syncthreads();
@@ -670,9 +681,12 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     float m = kNoMax, l = 0.f;
     unsigned vlim = kScaleLow;                                        // 4 bits: bound of the value scales met (bf16 bits)
     float vmul = kScaleTop * __uint_as_float((254u << 23) - (kScaleLow << 16));   // kScaleTop / bound
-    float acc[16][4];
+    // Sums over the rows, of column tile nt.  An item's products are summed apart and added by rounded additions: the
+    // tensor cores truncate what they add to, and over the hundreds of items of a long context that
+    // pulls sums towards zero (4e-6 at 1M rows).  High and residual rows meet here, so it is half the registers.
+    float acc[16][2];
 #pragma unroll
-    for (int nt = 0; nt < 16; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    for (int nt = 0; nt < 16; ++nt) acc[nt][0] = acc[nt][1] = 0.f;
 
 #pragma unroll 1
     for (; i < i_end; i += W) {
@@ -714,9 +728,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
             const float now = kScaleTop * __uint_as_float((254u << 23) - (vlim << 16)), by = now / vmul;
             vmul = now;
 #pragma unroll
-            for (int nt = 0; nt < 16; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[nt][i] *= by;
+            for (int nt = 0; nt < 16; ++nt) {
+              acc[nt][0] *= by;
+              acc[nt][1] *= by;
+            }
           }
         }
         kscale[128 * warp + lane] = bf16_lo(w.x);
@@ -743,7 +758,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
           const uint4 a0 = lds128(qf_a + 1024 * g4), a1 = lds128(qf_a + 1024 * g4 + 512);
-          const uint32_t a1r[4] = {a1.x, a1.y, a1.z, a1.w};
+          const uint32_t a0r[4] = {a0.x, a0.y, a0.z, a0.w}, a1r[4] = {a1.x, a1.y, a1.z, a1.w};
           const float2 centre = q8[8 * g4 + gid];
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -753,7 +768,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
               uint32_t c[4];
               float d[4];
               code_pairs(w, c);
-              mma16816_from(d, a0, c[0], c[1], centre);
+              mma16816_from<true>(d, a0r, c[0], c[1], centre);
               mma16816<true>(d, a1r, c[2], c[3]);
               const float2 k = *reinterpret_cast<const float2*>(kscale + 128 * warp + 32 * g4 + 16 * u + 8 * j + 2 * t4);
               p[u][j][0] = g4 == 0 ? k.x * (d[0] + d[2]) : fmaf(k.x, d[0] + d[2], p[u][j][0]);
@@ -811,9 +826,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         l *= alpha;
         m = mn;
 #pragma unroll
-        for (int nt = 0; nt < 16; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[nt][i] *= alpha;
+        for (int nt = 0; nt < 16; ++nt) {
+          acc[nt][0] *= alpha;
+          acc[nt][1] *= alpha;
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -826,42 +842,47 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
           }
       // ---- acc += P V
       if (kF16) {
+        uint2 vw[U][2][2];
+        __half2 ph[U][2], pl[U][2];
+        uint4 sv[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const unsigned char* vb = st + u * kBlk + kBlockTok * kRow4 + gid * 8;
-          uint2 vw[2][2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) vw[j][e] = *reinterpret_cast<const uint2*>(vb + (8 * j + 2 * t4 + e) * kRow4);
-          __half2 ph[2], pl[2];
-          uint32_t sv[2][4];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            split_f16(p[u][j][0], p[u][j][1], ph[j], pl[j]);
-            const uint4 v = vscale[16 * warp + 8 * u + 4 * j + t4];
-            sv[j][0] = v.x;
-            sv[j][1] = v.y;
-            sv[j][2] = v.z;
-            sv[j][3] = v.w;
+            const unsigned char* vb = st + u * kBlk + kBlockTok * kRow4 + gid * 8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) vw[u][j][e] = *reinterpret_cast<const uint2*>(vb + (8 * j + 2 * t4 + e) * kRow4);
+            split_f16(p[u][j][0], p[u][j][1], ph[u][j], pl[u][j]);
+            sv[u][j] = vscale[16 * warp + 8 * u + 4 * j + t4];
           }
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
+        for (int g4 = 0; g4 < 4; ++g4) {
+          float x[4][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
             uint32_t pa[4], w[2], c0[4], c1[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               // high part of the product; its exact rounding error and the low part make the residual
-              const __half2 sg = half2_of(sv[j][g4]);
-              const __half2 hi = __hmul2(ph[j], sg);
+              const __half2 sg = half2_of(g4 == 0 ? sv[u][j].x : g4 == 1 ? sv[u][j].y : g4 == 2 ? sv[u][j].z : sv[u][j].w);
+              const __half2 hi = __hmul2(ph[u][j], sg);
               pa[2 * j] = bits(hi);
-              pa[2 * j + 1] = bits(__hfma2(pl[j], sg, __hfma2(ph[j], sg, __hneg2(hi))));
-              w[j] = g4 < 2 ? __byte_perm(vw[j][0].x, vw[j][1].x, (g4 & 1) ? 0x7632 : 0x5410)
-                            : __byte_perm(vw[j][0].y, vw[j][1].y, (g4 & 1) ? 0x7632 : 0x5410);
+              pa[2 * j + 1] = bits(__hfma2(pl[u][j], sg, __hfma2(ph[u][j], sg, __hneg2(hi))));
+              w[j] = g4 < 2 ? __byte_perm(vw[u][j][0].x, vw[u][j][1].x, (g4 & 1) ? 0x7632 : 0x5410)
+                            : __byte_perm(vw[u][j][0].y, vw[u][j][1].y, (g4 & 1) ? 0x7632 : 0x5410);
             }
             centred_pairs(w[0], c0);
             centred_pairs(w[1], c1);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) mma16816<true>(acc[4 * g4 + t], pa, c0[t], c1[t]);
+            for (int t = 0; t < 4; ++t) {
+              if (u == 0) mma16816_from<true>(x[t], pa, c0[t], c1[t], make_float2(0.f, 0.f));
+              else mma16816<true>(x[t], pa, c0[t], c1[t]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            acc[4 * g4 + t][0] += x[t][0] + x[t][2];
+            acc[4 * g4 + t][1] += x[t][1] + x[t][3];
           }
         }
       } else {
@@ -894,11 +915,13 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
             bv[2] &= live0;
             bv[3] &= live1;
           }
-          mma16816<false>(acc[nt], pa, bv[0], bv[1]);
-          mma16816<false>(acc[nt + 1], pa, bv[2], bv[3]);
-          if (WIDE) {
-            mma16816<false>(acc[nt], pb, bv[0], bv[1]);
-            mma16816<false>(acc[nt + 1], pb, bv[2], bv[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x[4];
+            mma16816_from<false>(x, pa, bv[2 * i], bv[2 * i + 1], make_float2(0.f, 0.f));
+            if (WIDE) mma16816<false>(x, pb, bv[2 * i], bv[2 * i + 1]);
+            acc[nt + i][0] += x[0] + x[2];
+            acc[nt + i][1] += x[1] + x[3];
           }
         }
       }
@@ -912,8 +935,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     for (int nt = 0; nt < 16; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        o[nt][e] = acc[nt][e] + acc[nt][2 + e];
-        if (kF16) o[nt][e] *= ((nt & 1) ? kCodeUnit / 16.f : kCodeUnit) / vmul;
+        o[nt][e] = acc[nt][e];
+        if (kF16) o[nt][e] *= kValueUnit / vmul;
         else if (!WIDE) o[nt][e] += __shfl_xor_sync(kFull, o[nt][e], 16);
       }
     }
