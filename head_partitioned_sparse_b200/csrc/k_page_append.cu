@@ -286,12 +286,12 @@ __device__ __forceinline__ void round8(const float (&y)[8], float i0, float i1, 
 }
 
 template <typename T, int FMT, int PAIR>
-__global__ void __launch_bounds__(256, 2) k_page_append(const PagePool P, const AppendArgs a, const __grid_constant__ RopeTab128 tab) {
+__global__ void __launch_bounds__(128, 4) k_page_append(const PagePool P, const AppendArgs a, const __grid_constant__ RopeTab128 tab) {
   const int lane = threadIdx.x & 31;
   RowPair R;
   R.e = lane & 7;
   R.mask = 0xffu << (lane & 24);
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3;
+  const int64_t item = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 3;
   int hg, b, t;
   if (item >= (int64_t)a.B * a.T * a.head_groups) return;
   if (a.small) {   // 32-bit divisions where they suffice
@@ -469,9 +469,9 @@ __global__ void __launch_bounds__(256, 2) k_page_append(const PagePool P, const 
         kw[h] = pack_codes(q);
       }
     } else {
-      // A rotated value is off by at most 5e-7 m (|x| + |partner|): cos and sin by 1.6e-7 (argument and function)
+      // A rotated value is off by at most 3.5e-7 m (|x| + |partner|): cos and sin by 1.6e-7 (argument and function)
       // and 6e-8 (magnitude), the products and the sum by 6e-8 each.  NaN and infinity show here, too.
-      const float err = PAIR == kNone ? 0.f : __uint_as_float(xtop) * (5e-7f * fmaxf(mag, 1.f));
+      const float err = PAIR == kNone ? 0.f : __uint_as_float(xtop) * (3.5e-7f * fmaxf(mag, 1.f));
       float far = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -524,9 +524,9 @@ __device__ __forceinline__ void nibbles(unsigned w, float (&f)[8]) {
 // A warp takes 16 consecutive rows of one (sequence, head); a half-warp reads and writes whole
 // rows, all 8 row pairs in flight together.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(256) k_page_read(const PagePool P, const ReadArgs a) {
+__global__ void __launch_bounds__(128) k_page_read(const PagePool P, const ReadArgs a) {
   const int lane = threadIdx.x & 31, e = lane & 15;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int64_t unit = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 5;
   const int per_seq = (a.T + 15) / 16;
   const int64_t slice = unit / per_seq;
   if (slice >= (int64_t)a.B * P.Hkv) return;
@@ -597,10 +597,10 @@ __global__ void __launch_bounds__(256) k_page_read(const PagePool P, const ReadA
 
 template <typename T, int FMT>
 cudaError_t append_go(const PagePool& pool, const AppendArgs& a, const RopeTab128& tab, unsigned blocks, cudaStream_t st) {
-  if (tab.rot == 0) k_page_append<T, FMT, kNone><<<blocks, 256, 0, st>>>(pool, a, tab);
-  else if (tab.interleaved) k_page_append<T, FMT, kInLane><<<blocks, 256, 0, st>>>(pool, a, tab);
-  else if (tab.rot == kHeadDim) k_page_append<T, FMT, kWhole><<<blocks, 256, 0, st>>>(pool, a, tab);
-  else k_page_append<T, FMT, kFetch><<<blocks, 256, 0, st>>>(pool, a, tab);
+  if (tab.rot == 0) k_page_append<T, FMT, kNone><<<blocks, 128, 0, st>>>(pool, a, tab);
+  else if (tab.interleaved) k_page_append<T, FMT, kInLane><<<blocks, 128, 0, st>>>(pool, a, tab);
+  else if (tab.rot == kHeadDim) k_page_append<T, FMT, kWhole><<<blocks, 128, 0, st>>>(pool, a, tab);
+  else k_page_append<T, FMT, kFetch><<<blocks, 128, 0, st>>>(pool, a, tab);
   return cudaGetLastError();
 }
 
@@ -613,7 +613,7 @@ cudaError_t launch_page_append(const PagePool& pool, AppendArgs a, int dtype, in
   a.head_groups = (pool.Hkv + 7) / 8;
   while (a.head_groups < pool.Hkv && toks * a.head_groups * 8 < (int64_t)num_sms * 512) a.head_groups *= 2;
   if (a.head_groups > pool.Hkv) a.head_groups = pool.Hkv;
-  const int64_t blocks = (toks * a.head_groups * 8 + 255) / 256;
+  const int64_t blocks = (toks * a.head_groups * 8 + 127) / 128;
   a.small = toks * a.head_groups < INT32_MAX;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (dtype == 0)
@@ -625,15 +625,15 @@ cudaError_t launch_page_append(const PagePool& pool, AppendArgs a, int dtype, in
 
 cudaError_t launch_page_read(const PagePool& pool, const ReadArgs& a, int dtype, int format, cudaStream_t st) {
   const int64_t units = (int64_t)a.B * pool.Hkv * ((a.T + 15) / 16);
-  const int64_t blocks = (units * 32 + 255) / 256;
+  const int64_t blocks = (units * 32 + 127) / 128;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const unsigned nb = (unsigned)blocks;
   if (dtype == 0) {
-    if (format == kPageInt4) k_page_read<__nv_bfloat16, kPageInt4><<<nb, 256, 0, st>>>(pool, a);
-    else k_page_read<__nv_bfloat16, kPageBf16><<<nb, 256, 0, st>>>(pool, a);
+    if (format == kPageInt4) k_page_read<__nv_bfloat16, kPageInt4><<<nb, 128, 0, st>>>(pool, a);
+    else k_page_read<__nv_bfloat16, kPageBf16><<<nb, 128, 0, st>>>(pool, a);
   } else {
-    if (format == kPageInt4) k_page_read<float, kPageInt4><<<nb, 256, 0, st>>>(pool, a);
-    else k_page_read<float, kPageBf16><<<nb, 256, 0, st>>>(pool, a);
+    if (format == kPageInt4) k_page_read<float, kPageInt4><<<nb, 128, 0, st>>>(pool, a);
+    else k_page_read<float, kPageBf16><<<nb, 128, 0, st>>>(pool, a);
   }
   return cudaGetLastError();
 }

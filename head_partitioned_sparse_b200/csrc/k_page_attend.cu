@@ -10,7 +10,7 @@
 // time, a lane each (slice, page, byte offset, row mask), so the search, the division and the block
 // table cost 1/32 a unit, and those lanes start the copies: a block is one bulk copy (2304 bytes in 4
 // bits: K, V and scales together).  Listed units are gathered by 16-byte asynchronous copies, their
-// positions loaded two items ahead, their pages one.
+// positions loaded three items ahead, their pages two.
 // (Two producer warps for the whole CTA were measured 1.8 times slower: one lane's waits and copies in turn.)
 // Where the slices fit the CTAs well, every CTA's share lies in one slice: a share that straddles two
 // pays for their queries and their merge twice (about 4 us of 1.9 GHz).
@@ -341,11 +341,18 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
 #pragma unroll
       for (int i = 0; i < kLaneSlices; ++i) {
         const int s = lane * kLaneSlices + i;
+        // listed items weigh more: their gathering is worth 0.3 of an item (63 against 50 k cycles for the same number)
         n[i] = s < NS ? (float)(rpre[s + 1] - rpre[s]) : 0.f;
+        if (LISTED && s < NS) n[i] += 0.3f / (16 * U) * sinfo[s].y;
         top = fmaxf(top, n[i]);
       }
       top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
-      const float equal = __fdividef((float)T, (float)gridDim.x);
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < kLaneSlices; ++i) all += n[i];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+      const float equal = __fdividef(all, (float)gridDim.x);
       float most = fmaxf(equal, (float)W);
       int k[kLaneSlices], sum = 0;
 #pragma unroll 1
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     }
     return X;
   };
-  // `cur` holds the item to be issued; `nxt`, where it differs, the item two ahead of it (lists)
+  // `cur` holds the item to be issued; `nxt`, where it differs, the item two or three ahead of it (lists)
   Unit cur = find(0), nxt = cur;
   int ki = 0;   // the next item to issue
   auto list_rows = [&](int k) {   // starts the loads of item k's positions
@@ -512,11 +519,13 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     }
     R.id = __ldg(A.pool.table + (size_t)(R.bg >> 8) * A.pool.max_pages + page_of((unsigned)R.pos / kBlockTok));
   };
-  Rows r0, r1;   // of items ki and ki + 1
+  Rows r0, r1, r2;   // of items ki, ki + 1 (their pages loaded, too) and ki + 2
   if (LISTED) {
     r0 = list_rows(0);
-    list_pages(r0);
     r1 = list_rows(1);
+    r2 = list_rows(2);
+    list_pages(r0);
+    list_pages(r1);
   }
   int islot = 0;           // ring slot of item ki
   unsigned was_list = 0u;  // slots last written by gathers
@@ -582,12 +591,13 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     }
     if (LISTED) asm volatile("cp.async.commit_group;\n" ::: "memory");
     ++ki;
-    if (LISTED) {   // the items behind: found two early, for the lists' pipeline
-      if ((ki + 2) % kItems == 0) nxt = find(ki + 2);
+    if (LISTED) {   // the items behind: found three early, for the lists' pipeline
+      if ((ki + 3) % kItems == 0) nxt = find(ki + 3);
       if (ki % kItems == 0) cur = nxt;
       r0 = r1;
-      list_pages(r0);
-      r1 = list_rows(ki + 1);
+      r1 = r2;
+      list_pages(r1);
+      r2 = list_rows(ki + 2);
     } else if (ki % kItems == 0) {
       cur = find(ki);
     }
