@@ -10,7 +10,7 @@
 // time, a lane each (slice, page, byte offset, row mask), so the search, the division and the block
 // table cost 1/32 a unit, and those lanes start the copies: a block is one bulk copy (2304 bytes in 4
 // bits: K, V and scales together).  Listed units are gathered by 16-byte asynchronous copies, their
-// positions loaded three items ahead, their pages two.
+// positions loaded two items ahead, their pages one.
 // (Two producer warps for the whole CTA were measured 1.8 times slower: one lane's waits and copies in turn.)
 // Where the slices fit the CTAs well, every CTA's share lies in one slice: a share that straddles two
 // pays for their queries and their merge twice (about 4 us of 1.9 GHz).

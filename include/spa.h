@@ -520,7 +520,7 @@ SPA_API spa_status spa_paged_status(spa_paged* h, spa_stream stream);
  *   n_new_opt     NULL (T of every sequence), or device int64 [B] in [0, T]: a padded batch
  *   block_table   device int32 [B][max_pages]; only entries of written positions are read
  *   pages         device, 16-byte aligned; nothing but the new rows is written
- * A page that the call writes must not be another sequence's too. */
+ * A page that the call writes must not be another sequence's too, nor stand twice in its own. */
 SPA_API spa_status spa_kv_append_paged(spa_paged* h, const void* k_pre, const int64_t* k_strides, const void* v_new,
                       const int64_t* v_strides, const int64_t* start_pos, const int64_t* n_new_opt, int B, int T,
                       const int32_t* block_table, void* pages, spa_stream stream);
@@ -544,11 +544,12 @@ SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int3
  *   seq_lens   device int64 [B], 0..max_seq_len; a sequence of length 0 gives zeros
  *   max_seq_len  host bound; 0 = max_pages * page_size
  *   head_mask_opt  HOST uint8 [Hkv]; n_sink, window >= 0, n_sink + window >= 1 (read only with a mask)
- *   sel_idx_opt, sel_count_opt  device int32 [B][Hkv][sel_stride] and [B * Hkv]; both or neither
+ *   sel_idx_opt, sel_count_opt  device int32 [B][Hkv][sel_stride] and [B * Hkv]; both or neither (with a mask);
+ *              1 <= sel_stride <= 2^30
  *   out        device float32 [B][Hq][128]; lse_opt NULL or device float32 [B][Hq]: log2 of the softmax
  *              denominator (-infinity for zeros), as spa_cp_combine takes it
- * Queries and probabilities are kept to about 17 bits for the tensor cores, sums in float32; the result does
- * not depend on timing.  Masked rows contribute nothing, whatever their bytes. */
+ * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32; the
+ * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes. */
 SPA_API spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, const int32_t* block_table,
                       const int64_t* seq_lens, int B, int64_t max_seq_len, const uint8_t* head_mask_opt, int n_sink,
                       int window, const int32_t* sel_idx_opt, const int32_t* sel_count_opt, int64_t sel_stride,
