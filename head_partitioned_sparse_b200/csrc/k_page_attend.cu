@@ -277,9 +277,9 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     bool big = false;
     for (int base = 0; base < NS; base += W * 32) {
       const int s = base + tid;
-      long long n = 0;
+      int n = 0;
       if (s < NS) {
-        const int b = s / Hkv, g = s - b * Hkv;
+        const int b = Hkv == 1 ? s : (int)__umulhi((unsigned)s, A.by_heads), g = s - b * Hkv;
         int64_t L = A.seq_lens[b];
         if (L < 0 || L > A.cap) {
           atomicOr(A.pool.err, kErrSeqLen);
@@ -297,10 +297,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         n = (units_of(make_slice(A, g, (int)L, cnt)) + U - 1) / U;
         big = big || n > 2 * W;
       }
-      long long v = n;
+      int v = n;   // 32 slices of 2^21 units at most
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, v, o);
+        const int y = __shfl_up_sync(kFull, v, o);
         if (lane >= o) v += y;
       }
       if (lane == 31) shl[warp] = v;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   // ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice; taken where its
   // largest share is within kPieceItems of the equal share: what a second slice would cost a CTA.  Else
   // equal shares, down to one item a CTA.
-  constexpr int kLaneSlices = 5, kPieceItems = 12;
+  constexpr int kLaneSlices = 5, kPieceItems = 24;
   if (!small) {
     if (NS > 32 * kLaneSlices || NS > (int)gridDim.x) {
       if (tid == 0) s_split = make_int4(0, 0, -1, 0);
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         }
         sum = __reduce_add_sync(kFull, mine);
         if (sum <= (int)gridDim.x) break;
-        most = t == 7 ? top * 1.0001f : fmaxf(most * __fdividef((float)sum, (float)gridDim.x), most * 1.01f);
+        most = t == 7 ? top * 1.0001f : fminf(fmaxf(most * __fdividef((float)sum, (float)gridDim.x), most * 1.01f), top * 1.0001f);
       }
       float share = 0.f;
       int mine = 0;

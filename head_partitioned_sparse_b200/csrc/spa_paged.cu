@@ -381,8 +381,8 @@ spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, 
   if ((sel_idx_opt != nullptr) != (sel_count_opt != nullptr))
     return fail(SPA_ERR_INVALID_ARG, "sel_idx and sel_count come together");
   if (sel_idx_opt && !head_mask_opt) return fail(SPA_ERR_INVALID_ARG, "a selection needs the head mask");
-  if (sel_idx_opt && (!aligned(sel_idx_opt, 4) || !aligned(sel_count_opt, 4) || sel_stride < 1 || sel_stride > (1 << 30)))
-    return fail(SPA_ERR_INVALID_ARG, "sel_idx and sel_count must be 4-byte aligned, sel_stride in [1, 2^30] (got %lld)",
+  if (sel_idx_opt && (!aligned(sel_idx_opt, 4) || !aligned(sel_count_opt, 4) || sel_stride < 1 || sel_stride > spa::kMaxCtx))
+    return fail(SPA_ERR_INVALID_ARG, "sel_idx and sel_count must be 4-byte aligned, sel_stride in [1, 2^24] (got %lld)",
                 (long long)sel_stride);
   if (head_mask_opt && (n_sink < 0 || window < 0 || (int64_t)n_sink + window < 1))
     return fail(SPA_ERR_INVALID_ARG, "n_sink, window must be >= 0 with n_sink + window >= 1");

@@ -545,7 +545,7 @@ SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int3
  *   max_seq_len  host bound; 0 = max_pages * page_size
  *   head_mask_opt  HOST uint8 [Hkv]; n_sink, window >= 0, n_sink + window >= 1 (read only with a mask)
  *   sel_idx_opt, sel_count_opt  device int32 [B][Hkv][sel_stride] and [B * Hkv]; both or neither (with a mask);
- *              1 <= sel_stride <= 2^30
+ *              1 <= sel_stride <= 2^24
  *   out        device float32 [B][Hq][128]; lse_opt NULL or device float32 [B][Hq]: log2 of the softmax
  *              denominator (-infinity for zeros), as spa_cp_combine takes it
  * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32; the

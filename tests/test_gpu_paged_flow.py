@@ -341,7 +341,7 @@ def test_a_mask_of_the_wrong_length_and_host_tensors_are_refused():
         for kw in (dict(max_seq_len=-1), dict(max_seq_len=33), dict(B=2), dict(B=0), dict(sel_idx=c.table),
                    dict(sel_idx=c.table, sel_count=c.table), dict(head_mask=b"\0\1"), dict(head_mask=b"\0\1", n_sink=-1, window=5),
                    dict(head_mask=b"\0\1", window=1, sel_idx=c.table, sel_count=c.table, sel_stride=0),
-                   dict(head_mask=b"\0\1", window=1, sel_idx=c.table, sel_count=c.table, sel_stride=(1 << 30) + 1)):
+                   dict(head_mask=b"\0\1", window=1, sel_idx=c.table, sel_count=c.table, sel_stride=(1 << 24) + 1)):
             a = {**dict(B=1, max_seq_len=0), **kw}
             with pytest.raises(B.SpaError) as e:
                 B.spa_attend_paged(c.h, q, c.pages, c.table, c.n, a.pop("B"), a.pop("max_seq_len"), out, **a)
