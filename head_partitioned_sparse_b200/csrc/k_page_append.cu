@@ -279,9 +279,9 @@ __device__ __forceinline__ bool scale_unsure(float u, float s, float err) {
 __device__ __forceinline__ void round8(const float (&y)[8], float i0, float i1, float (&t)[8], float& far) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = y[i] * (i < 4 ? i0 : i1);
-    t[i] = q + kMagic;
-    far = fmaxf(far, fabsf(q - (t[i] - kMagic)));
+    const float inv = i < 4 ? i0 : i1;
+    t[i] = fmaf(y[i], inv, kMagic);
+    far = fmaxf(far, fabsf(fmaf(y[i], inv, kMagic - t[i])));
   }
 }
 
@@ -521,6 +521,21 @@ __device__ __forceinline__ void nibbles(unsigned w, float (&f)[8]) {
   for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x4b000000u | ((w >> (4 * i)) & 15u)) - 8388616.f;
 }
 
+// 8 codes as bf16: 128 + n by its bits, less 136, times the scale (dims 0-3, dims 4-7): one rounding, of the exact product.
+__device__ __forceinline__ uint4 expand_bf16(unsigned w, uint32_t s0, uint32_t s1) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // nibbles i and i + 4
+    r[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0xc308c308u));   // -136
+  }
+  uint32_t o[4] = {__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410), __byte_perm(r[0], r[1], 0x7632),
+                   __byte_perm(r[2], r[3], 0x7632)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(i < 2 ? s0 : s1));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // A warp takes 16 consecutive rows of one (sequence, head); a half-warp reads and writes whole
 // rows, all 8 row pairs in flight together.
 template <typename T, int FMT>
@@ -569,6 +584,14 @@ __global__ void __launch_bounds__(128) k_page_read(const PagePool P, const ReadA
   for (int u = 0; u < 8; ++u) {
     if (base[u] < 0) continue;
     const int i = i0 + 2 * u + (lane >> 4);
+    if constexpr (FMT == kPageInt4 && sizeof(T) == 2) {
+      const unsigned kg = (e & 2) ? sc[u].y : sc[u].x, vg = (e & 1) ? sc[u].w : sc[u].z;
+      const uint32_t s = __byte_perm(kg, kg, (e & 1) ? 0x3232 : 0x1010);
+      *reinterpret_cast<uint4*>(kd + i * a.ks.t + 8 * e) = expand_bf16(kw[u], s, s);
+      *reinterpret_cast<uint4*>(vd + i * a.vs.t + 8 * e) =
+          expand_bf16(vw[u], __byte_perm(vg, vg, 0x1010), __byte_perm(vg, vg, 0x3232));
+      continue;
+    }
     float k[8], v[8];
     if (FMT == kPageInt4) {
       nibbles(kw[u], k);
