@@ -11,9 +11,9 @@
 // table cost 1/32 a unit, and those lanes start the copies: a block is one bulk copy (2304 bytes in 4
 // bits: K, V and scales together).  Listed units are gathered by 16-byte asynchronous copies, their
 // positions loaded two items ahead, their pages one.
-// (Two producer warps for the whole CTA were measured 1.8 times slower: one lane's waits and copies in turn.)
+// (Two producer warps for the whole CTA took 737 us for 1M rows where this took 411: one lane's waits and copies in turn.)
 // Where the slices fit the CTAs well, every CTA's share lies in one slice: a share that straddles two
-// pays for their queries and their merge twice (about 4 us of 1.9 GHz).
+// pays for their queries and their merge twice.
 // Warps keep their own running maximum and sum, merged in a fixed order at the end of a slice's piece;
 // the last CTA to finish a slice (a ticket) merges the CTAs' states in order, so the result does
 // not depend on timing.
@@ -329,9 +329,13 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   }
   // ---- shares.  A CTA a slice where those are small and few.  Else aligned to slices: a slice of n items takes
   // ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice; taken where its
-  // largest share is within kPieceItems of the equal share: what a second slice would cost a CTA.  Else
-  // equal shares, down to one item a CTA.
+  // largest share is within kPieceItems or 0.3 of the equal share: what a second slice would cost a CTA.  Else
+  // equal shares, down to one item a CTA.  us with equal shares against aligned ones: one sequence of 4096 rows 19.4 /
+  // 14.1, 16 of them 37.4 / 32.7, 4 x 128K with lists 55.2 / 51.6; but 16 x 64K of bf16, a quarter of the heads
+  // seeing every row, 134 / 429.  Limits of 24 items alone, 0.3, 0.6: 5 x 64K of those 64.7 / 60.4 / 60.4,
+  // 9 x 128K with lists 83.7 / 83.7 / 94.4.
   constexpr int kLaneSlices = 5, kPieceItems = 24;
+  constexpr float kUneven = 0.3f;
   if (!small) {
     if (NS > 32 * kLaneSlices || NS > (int)gridDim.x) {
       if (tid == 0) s_split = make_int4(0, 0, -1, 0);
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
 #pragma unroll
       for (int i = 0; i < kLaneSlices; ++i) {
         const int s = lane * kLaneSlices + i;
-        // listed items weigh more: their gathering is worth 0.3 of an item (63 against 50 k cycles for the same number)
+        // listed items weigh more: their gathering is worth 0.3 of an item (4 x 128K with lists: 55.0 us without, 51.6 with)
         n[i] = s < NS ? (float)(rpre[s + 1] - rpre[s]) : 0.f;
         if (LISTED && s < NS) n[i] += 0.3f / (16 * U) * sinfo[s].y;
         top = fmaxf(top, n[i]);
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         if (lane >= o) before += y;
       }
       before -= mine;
-      const bool fits = sum <= (int)gridDim.x && share <= equal + kPieceItems;
+      const bool fits = sum <= (int)gridDim.x && share <= equal + fmaxf((float)kPieceItems, kUneven * equal);
       if (lane == 0) s_split = make_int4(0, 0, fits ? 0 : -1, 0);
       __syncwarp();
       if (fits) {
@@ -1076,45 +1080,47 @@ constexpr size_t smem_bytes(int n_slices) {
          (size_t)(n_slices + 1) * 8 + (size_t)n_slices * 8;
 }
 constexpr size_t smem_most(int format) { return (format == kPageInt4 ? 212 : 226) * 1024; }   // 227 KB less the static arrays
-// Warps, units an item, ring slots; the deeper ring where the slices' prefix leaves room for it.
-constexpr int kW4 = 12, kU4 = 2, kS4 = 3, kS4Many = 2;
-constexpr int kW16 = 8, kU16 = 1, kS16 = 3, kS16Many = 2;
+// Warps and units an item.  Ring slots: 2, and 3 for 4-bit calls without lists where the slices' prefix leaves room.
+// us with 2 slots against 3: 1M rows of 4 bits 359 / 344; 4 x 128K with lists 50.1 / 51.6; 16 x 64K of bf16 127 / 134.
+constexpr int kW4 = 12, kU4 = 2;
+constexpr int kW16 = 8, kU16 = 1;
+constexpr int kSlots = 2, kDeep4 = 3;
 
 template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
 bool setup_one() {
   return cudaFuncSetAttribute(k_attend_paged<FMT, W, U, S, WIDE, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)smem_most(FMT)) == cudaSuccess;
 }
-template <int FMT, int W, int U, int S, int SMANY, bool WIDE>
+template <int FMT, int W, int U, bool WIDE>
 bool setup() {
-  static_assert(smem_bytes<FMT, W, U, SMANY>(kMaxPagedSlices) <= smem_most(FMT), "the shallow ring fits every call");
-  return setup_one<FMT, W, U, S, WIDE, false>() && setup_one<FMT, W, U, S, WIDE, true>() &&
-         setup_one<FMT, W, U, SMANY, WIDE, false>() && setup_one<FMT, W, U, SMANY, WIDE, true>();
+  static_assert(smem_bytes<FMT, W, U, kSlots>(kMaxPagedSlices) <= smem_most(FMT), "two slots fit every call");
+  return setup_one<FMT, W, U, kSlots, WIDE, false>() && setup_one<FMT, W, U, kSlots, WIDE, true>();
 }
-template <int FMT, int W, int U, int S, bool WIDE>
-void launch(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
-  const size_t n = smem_bytes<FMT, W, U, S>(a.n_slices);
-  if (a.list) k_attend_paged<FMT, W, U, S, WIDE, true><<<grid, W * 32, n, st>>>(a, tab);
-  else k_attend_paged<FMT, W, U, S, WIDE, false><<<grid, W * 32, n, st>>>(a, tab);
-}
-template <int FMT, int W, int U, int S, int SMANY, bool WIDE>
-cudaError_t go(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
-  if (smem_bytes<FMT, W, U, S>(a.n_slices) <= smem_most(FMT)) launch<FMT, W, U, S, WIDE>(a, grid, tab, st);
-  else launch<FMT, W, U, SMANY, WIDE>(a, grid, tab, st);
+template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
+cudaError_t launch(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
+  k_attend_paged<FMT, W, U, S, WIDE, LISTED><<<grid, W * 32, smem_bytes<FMT, W, U, S>(a.n_slices), st>>>(a, tab);
   return cudaGetLastError();
+}
+template <int FMT, int W, int U, bool WIDE>
+cudaError_t go(const PagedAttendArgs& a, int grid, const RopeTab128& tab, cudaStream_t st) {
+  return a.list ? launch<FMT, W, U, kSlots, WIDE, true>(a, grid, tab, st)
+                : launch<FMT, W, U, kSlots, WIDE, false>(a, grid, tab, st);
 }
 
 }  // namespace
 
 int page_attend_setup(int format) {
-  if (format == kPageInt4) return setup<kPageInt4, kW4, kU4, kS4, kS4Many, false>();
-  return setup<kPageBf16, kW16, kU16, kS16, kS16Many, false>() && setup<kPageBf16, kW16, kU16, kS16, kS16Many, true>();
+  if (format == kPageInt4) return setup<kPageInt4, kW4, kU4, false>() && setup_one<kPageInt4, kW4, kU4, kDeep4, false, false>();
+  return setup<kPageBf16, kW16, kU16, false>() && setup<kPageBf16, kW16, kU16, true>();
 }
 
 cudaError_t launch_page_attend(const PagedAttendArgs& a, int format, int grid, const RopeTab128& tab, cudaStream_t st) {
-  if (format == kPageInt4) return go<kPageInt4, kW4, kU4, kS4, kS4Many, false>(a, grid, tab, st);
-  return a.G <= 4 ? go<kPageBf16, kW16, kU16, kS16, kS16Many, false>(a, grid, tab, st)
-                  : go<kPageBf16, kW16, kU16, kS16, kS16Many, true>(a, grid, tab, st);
+  if (format == kPageInt4) {
+    if (!a.list && smem_bytes<kPageInt4, kW4, kU4, kDeep4>(a.n_slices) <= smem_most(kPageInt4))
+      return launch<kPageInt4, kW4, kU4, kDeep4, false, false>(a, grid, tab, st);
+    return go<kPageInt4, kW4, kU4, false>(a, grid, tab, st);
+  }
+  return a.G <= 4 ? go<kPageBf16, kW16, kU16, false>(a, grid, tab, st) : go<kPageBf16, kW16, kU16, true>(a, grid, tab, st);
 }
 
 }  // namespace spa
