@@ -76,12 +76,17 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for a phase to end, for two seconds at most.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity) {
+// Waits for a phase to end, for two seconds at most; for 100 us once a wait of the CTA has run out (*late): the phases
+// behind a missing copy do not match any more, and two seconds an item would not end.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, volatile int* late) {
   if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
-  while (!mbar_try(bar, parity))
-    if (now_ns() - t0 > 2000000000ull) return false;
+  while (!mbar_try(bar, parity)) {
+    if (now_ns() - t0 > (*late ? 100000ull : 2000000000ull)) {
+      *late = 1;
+      return false;
+    }
+  }
   return true;
 }
 __device__ __forceinline__ uint64_t l2_evict_first() {
@@ -252,6 +257,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   __shared__ unsigned vmask[W * S * U];   // attended rows of a slot's units; bit 16: gathered
   __shared__ long long shl[W];
   __shared__ int s_merge;
+  __shared__ int s_late;                       // a wait has run out
   __shared__ float qun[kMaxGroup];             // 4 bits: what a head's scores are multiplied by
   __shared__ int4 s_split;                     // aligned shares: slice, its first CTA, its CTAs, -1: equal shares
   __shared__ uint4 qf[kF16 ? 8 * 32 : 1];      // 4 bits: query operands, a lane's 16 bytes of each k-step
@@ -264,6 +270,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   const int NS = A.n_slices, Hkv = A.pool.Hkv, G = A.G;
 
   if (tid < W * S) mbar_init(smem_u32(&full[tid]), U);
+  if (tid == 0) s_late = 0;
   if (kF16) {   // heads that the group does not have
     if (tid < 256) qf[kF16 ? tid : 0] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 32) q8[kF16 ? tid : 0] = make_float2(0.f, 0.f);
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       __syncwarp();
       issue();   // refills the slot consumed last time
       const unsigned char* const st = ring + (warp * S + slot) * U * kBlk;
-      if (!mbar_wait(bar_a + 8 * slot, phase) && lane == 0) atomicOr(A.pool.err, kErrTimeout);
+      if (!mbar_wait(bar_a + 8 * slot, phase, &s_late) && lane == 0) atomicOr(A.pool.err, kErrTimeout);
       unsigned vm[U], any = 0u, all = 0xffffu;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
