@@ -11,7 +11,7 @@ import torch
 
 import paged_model as M
 from head_partitioned_sparse_b200 import binding as B
-from test_gpu_paged import FMT, KDT, TDT, Rope, f64, i64
+from test_gpu_paged import FMT, KDT, TDT, Rope, f64, i64, rope_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -351,3 +351,37 @@ def test_a_mask_of_the_wrong_length_and_host_tensors_are_refused():
         with pytest.raises(B.SpaError):
             B.spa_kv_append_paged(c.h, c.k, c.v, c.zero, 1, 1, c.table, c.pages, k_strides=(128, 128, 4))
         B.spa_paged_status(c.h)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_attend_shares_of_unequal_length(fmt):
+    """40 slices over the GPU's CTAs, 3 each: the largest share is a quarter above the equal one, yet whole slices."""
+    lens, Hq, Hkv = [14000, 14001, 13990, 14000, 13985], 32, 8
+    with Rope() as r, Cache(lens, Hq, Hkv, fmt, 16, "bf16", r) as c:
+        q = queries(c, seed=3)
+        out = torch.full((c.B, Hq, 128), float("nan"), device="cuda")
+        lse = torch.full((c.B, Hq), float("nan"), device="cuda")
+        B.spa_attend_paged(c.h, q, c.pages, c.table, c.n, c.B, 0, out, lse=lse)
+        B.spa_paged_status(c.h)
+        c.check(q, out, lse)
+
+
+@pytest.mark.parametrize("H,T,dtype,rot,layout", [
+    (40, 64, "bf16", 128, "interleaved"),   # 2 heads a thread
+    (9, 61, "bf16", 128, "half"),           # groups clipped to the heads
+    (33, 100, "bf16", 64, "half"),          # some threads with a head more than others
+    (12, 700, "f32", 36, "half"),
+    (8, 1, "f32", 128, "interleaved"),
+])
+def test_rope_heads_shared_among_threads(H, T, dtype, rot, layout):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn((1, T, H, 128), generator=g, device="cuda").to(TDT[dtype])
+    y = torch.full_like(x, float("nan"))
+    st = (T * H * 128, H * 128, 128)
+    with Rope(rot, layout, "plain") as r:
+        B.spa_rope_apply(r.h, x, y, 1, T, H, 128, KDT[dtype], start_pos=i64([70001]), x_strides=st, y_strides=st)
+        xs = f64(x).transpose(0, 2, 1, 3)
+        want = M.rotate(xs, 70001.0 + np.arange(T)[None, None, :], **r.model)
+    got = f64(y).transpose(0, 2, 1, 3)
+    assert (np.abs(got - want) <= rope_bound(xs, want, dtype, 1.0)).all()
+    assert np.array_equal(got[..., rot:], xs[..., rot:])
