@@ -36,6 +36,7 @@
 //     Rows come by matrix loads from the swizzled block.
 //
 // Masked rows: their score is -infinity and their value scale (bf16: their value) 0, whatever the page holds there.
+#include <cfloat>
 #include <climits>
 
 #include <cuda_fp16.h>
@@ -78,8 +79,8 @@ __device__ __forceinline__ unsigned long long now_ns() {
 }
 // Waits for a phase to end, for two seconds at most; for 100 us once a wait of the CTA has run out (*late): the phases
 // behind a missing copy do not match any more, and two seconds an item would not end.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, volatile int* late) {
-  if (mbar_try(bar, parity)) return true;
+// Out of line where it really waits: inlined, the loop's registers cost 1M rows 356 us in place of 347.
+__device__ __noinline__ bool mbar_wait_on(uint32_t bar, unsigned parity, volatile int* late) {
   const unsigned long long t0 = now_ns();
   while (!mbar_try(bar, parity)) {
     if (now_ns() - t0 > (*late ? 100000ull : 2000000000ull)) {
@@ -88,6 +89,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, volatil
     }
   }
   return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, volatile int* late) {
+  return mbar_try(bar, parity) || mbar_wait_on(bar, parity, late);
 }
 __device__ __forceinline__ uint64_t l2_evict_first() {
   uint64_t p;
@@ -336,11 +340,12 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   }
   // ---- shares.  A CTA a slice where those are small and few.  Else aligned to slices: a slice of n items takes
   // ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice; taken where its
-  // largest share is within kPieceItems or 0.3 of the equal share: what a second slice would cost a CTA.  Else
-  // equal shares, down to one item a CTA.  us with equal shares against aligned ones: one sequence of 4096 rows 19.4 /
-  // 14.1, 16 of them 37.4 / 32.7, 4 x 128K with lists 55.2 / 51.6; but 16 x 64K of bf16, a quarter of the heads
-  // seeing every row, 134 / 429.  Limits of 24 items alone, 0.3, 0.6: 5 x 64K of those 64.7 / 60.4 / 60.4,
-  // 9 x 128K with lists 83.7 / 83.7 / 94.4.
+  // largest share exceeds the equal one by no more than the slices passed through would cost a CTA: kPieceItems for a second,
+  // as much again where some slice is shorter than a share (a CTA then meets three).  Over bf16 pages, where memory bounds the
+  // call and a few idle CTAs cost little, by 0.3 of it too.  Else equal shares, down to one item a CTA.  us with equal shares against aligned ones: one sequence of 4096 rows 19.4 /
+  // 14.1, 16 of them 37.4 / 32.7, 4 x 128K with lists 55.2 / 51.6, 3 x 128K with half of the heads streaming 80.7 / 75.8; but 1M rows
+  // of 8 heads 344 / 348, and 16 x 64K of bf16, a quarter of the heads seeing every row, 134 / 429.  5 x 64K of those
+  // with a limit of 24 items, 0.3, 0.6: 64.7 / 60.4 / 60.4; 9 x 128K with lists, 4 bits: 83.7 / 83.7 / 94.4.
   constexpr int kLaneSlices = 5, kPieceItems = 24;
   constexpr float kUneven = 0.3f;
   if (!small) {
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       if (tid == 0) s_split = make_int4(0, 0, -1, 0);
     } else if (warp == 0) {
       float n[kLaneSlices];
-      float top = 0.f;
+      float top = 0.f, low = FLT_MAX;
 #pragma unroll
       for (int i = 0; i < kLaneSlices; ++i) {
         const int s = lane * kLaneSlices + i;
@@ -356,8 +361,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         n[i] = s < NS ? (float)(rpre[s + 1] - rpre[s]) : 0.f;
         if (LISTED && s < NS) n[i] += 0.3f / (16 * U) * sinfo[s].y;
         top = fmaxf(top, n[i]);
+        if (n[i] > 0.f) low = fminf(low, n[i]);
       }
       top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+      low = __uint_as_float(__reduce_min_sync(kFull, __float_as_uint(low)));
       float all = 0.f;
 #pragma unroll
       for (int i = 0; i < kLaneSlices; ++i) all += n[i];
@@ -394,7 +401,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         if (lane >= o) before += y;
       }
       before -= mine;
-      const bool fits = sum <= (int)gridDim.x && share <= equal + fmaxf((float)kPieceItems, kUneven * equal);
+      const float more = low < equal ? 2.f * kPieceItems : (float)kPieceItems;
+      const bool fits = sum <= (int)gridDim.x && share <= equal + (kF16 ? more : fmaxf(more, kUneven * equal));
       if (lane == 0) s_split = make_int4(0, 0, fits ? 0 : -1, 0);
       __syncwarp();
       if (fits) {
