@@ -47,7 +47,7 @@ namespace spa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kNoMax = -1e30f;        // running maximum before the first row
+constexpr float kNoMax = -FLT_MAX;     // running maximum before the first row: no score is below it
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, unsigned n) {

@@ -549,8 +549,8 @@ SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int3
  *   out        device float32 [B][Hq][128]; lse_opt NULL or device float32 [B][Hq]: log2 of the softmax
  *              denominator (-infinity for zeros), as spa_cp_combine takes it
  * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32; the
- * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes; nor do rows whose score (log2
- * e included) is below -1e30. */
+ * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes.  Scores (log2 e included) must
+ * lie within float32's range; one below it has no weight. */
 SPA_API spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, const int32_t* block_table,
                       const int64_t* seq_lens, int B, int64_t max_seq_len, const uint8_t* head_mask_opt, int n_sink,
                       int window, const int32_t* sel_idx_opt, const int32_t* sel_count_opt, int64_t sel_stride,

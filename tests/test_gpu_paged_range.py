@@ -1,0 +1,113 @@
+"""Attention over pages where its number formats could give out: scores far from 1, values and queries whose
+magnitudes differ from row to row, group to group and head to head, and the precision it documents.
+
+The bound.  A score is sum_g s_g sum_{d in g} q_d (n_d + 8) - 8 sum_d q_d over the scale groups g.  Queries are kept to 22
+bits (2^-22 relative), the tensor cores' sums of a group's 32 products are off by at most 2^-21 of the largest term for
+each of two products, float32 adds 2^-22 for the four groups: together at most 2^-20 of sum_d |q_d| 8 s_g(d), in units
+of the score.  Over bf16 pages 8 s is |k| (24 bits, eight products of 2^-21 in two chains: 2^-19 of sum |q k|).  A weight is then off by
+twice the largest score's error, relative, its own 2^-22 and the exponential's; an item's sums by 2^-21, the sums over
+the items by 2^-24 each: 2^-19 + items 2^-24 of sum p |v|."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_model as M
+from head_partitioned_sparse_b200 import binding as B
+from test_gpu_paged import f64, i64
+from test_gpu_paged_flow import Cache
+
+pytestmark = pytest.mark.gpu
+
+GK = torch.from_numpy(M.GROUP_K).long()
+
+
+def attend(c, q, lse=None):
+    out = torch.full((c.B, c.Hq, 128), float("nan"), device="cuda")
+    B.spa_attend_paged(c.h, q, c.pages, c.table, c.n, c.B, 0, out, lse=lse)
+    B.spa_paged_status(c.h)
+    return out
+
+
+def scales_k(c, b, g, n):
+    """Bounds 8 s of the stored keys' scales, by dim: of the codes' largest magnitude, 7 at most (and 4 at least, since the
+    group's largest value is 7 steps long but for the scale's rounding)."""
+    k = c.kr[b, g, :n].double().abs()
+    top = torch.stack([k[:, GK.cuda() == i].amax(-1) for i in range(4)], -1)
+    return (8 / 6 * top)[:, GK.cuda()]
+
+
+def reference(c, q, fmt):
+    """(want, bound, log2 denominators, their bound) of every head, float64 on the GPU; c without a rotation."""
+    G = c.Hq // c.Hkv
+    q64 = q.double()
+    want, bound = torch.zeros(2, c.B, c.Hq, 128, device="cuda", dtype=torch.float64).unbind(0)
+    lse, lb = torch.zeros(2, c.B, c.Hq, device="cuda", dtype=torch.float64).unbind(0)
+    for b in range(c.B):
+        L = c.lens[b]
+        for g in range(c.Hkv):
+            k, v = c.kr[b, g, :L].double(), c.vr[b, g, :L].double()
+            qq = q64[b, g * G:(g + 1) * G]
+            s = qq @ k.T / math.sqrt(128)
+            if fmt == "int4":
+                off = (qq.abs() @ scales_k(c, b, g, L).T / math.sqrt(128)).amax(-1) * 2.0 ** -20
+            else:
+                off = (qq.abs() @ k.abs().T / math.sqrt(128)).amax(-1) * 2.0 ** -19
+            m = s.amax(-1, keepdim=True)
+            p = torch.exp(s - m)
+            z = p.sum(-1, keepdim=True)
+            h = slice(g * G, (g + 1) * G)
+            want[b, h] = p @ v / z
+            bound[b, h] = (2 * off[:, None] + 2.0 ** -19 + -(-L // 16) * 2.0 ** -24) * (p @ v.abs() / z)
+            lse[b, h] = ((m + z.log()) / math.log(2.0))[:, 0]
+            # the maximum and the sum in float32, and the score's own error
+            lb[b, h] = 1.45 * 2 * off + 2.0 ** -22 * lse[b, h].abs() + 2.0 ** -18
+    return want, bound, lse, lb
+
+
+def check(c, q, fmt, dims=slice(None)):
+    lse = torch.full((c.B, c.Hq), float("nan"), device="cuda")
+    out = attend(c, q, lse)
+    want, bound, wl, lb = reference(c, q, fmt)
+    err = (out.double() - want).abs()
+    ok = err <= bound
+    assert ok[..., dims].all(), float((err / bound)[..., dims].nan_to_num(1e9).max())
+    assert ((lse.double() - wl).abs() <= lb).all()
+    return out, want
+
+
+# ------------------------------------------------------------------------------------------------ scores
+def signs(seed):
+    return torch.randint(0, 2, (128,), generator=torch.Generator().manual_seed(seed)).float().mul(2).sub(1).cuda()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_rows_far_below_each_other(fmt):
+    """One row takes all the weight: at the front, at the end, alone in its sequence; scores down to -1e37."""
+    L, G = 70, 2
+    e = torch.tensor([1e4, 1e9, 1e14, 3e16, 1e18], device="cuda")
+    n = len(e)
+    for at in (0, 35, L - 1, None):
+        k = -(e * torch.ones(1, device="cuda"))[:, None, None, None] * signs(3).expand(n, 1, L, 128)
+        v = torch.randn(n, 1, L, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+        q = (e[:, None, None] * signs(3).expand(n, G, 128)).contiguous()
+        lens = [1] * n
+        if at is not None:
+            lens = [L] * n
+            k[:, :, at] *= 0.5
+        with Cache(lens, G, 1, fmt, 16, "f32", k=k.contiguous(), v=v) as c:
+            out = attend(c, q)
+            row = c.vr[:, :, at or 0]
+            assert ((out - row).abs() <= 2.0 ** -19 * row.abs()).all()
+
+
+# ------------------------------------------------------------------------------------------------ values
+def unit_cache(seed, n, Hkv, L, fmt, lens=None, change=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.randn(n, Hkv, L, 128, generator=g, device="cuda")
+    v = torch.randn(n, Hkv, L, 128, generator=g, device="cuda")
+    q = 1.5 * torch.randn(n, Hkv * 4, 128, generator=g, device="cuda")
+    if change:
+        change(q, k, v)
+    return q, Cache(lens or [L] * n, 4 * Hkv, Hkv, fmt, 16, "f32", k=k, v=v)
