@@ -21,7 +21,7 @@
 // Matrix mapping (mma.sync m16n8k16, float32 sums).  The 16 rows of the operand hold the group's heads more
 // than once, as a high part and residuals, so that no bits of queries and probabilities are lost:
 //   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
-//     to a maximum of 2^10 a head; probabilities are 2^11 times their value and value scales at most 2^4
+//     to a maximum of 2^10 a head; probabilities are 2^11 times their value at most and value scales at most 2^4
 //     by the largest scale the warp has met (a power of two, moved like the running maximum), so
 //     float16's range holds both.  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
@@ -196,7 +196,7 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-constexpr float kProbExp = 11.f;         // 4 bits: probabilities are 2^11 times their value
+constexpr float kProbExp = 11.f;         // 4 bits: probabilities are 2^11 times their value (less where scores' steps are coarser)
 constexpr float kScaleTop = 16.f;        // 4 bits: value scales in float16, at most this
 constexpr unsigned kScaleLow = 0x0d80u;  // bf16 2^-100: the least bound of the value scales
 
@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         for (int j = 0; j < 2; ++j) mx = fmaxf(mx, fmaxf(p[u][j][0], p[u][j][1]));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const float mn = fmaxf(m, fmaf(mx, unscale, kF16 ? -kProbExp : 0.f));
+      // rounded up: where 11 is less than a step of the score, a rounding down would let the top probability past 2^11
+      const float mn = fmaxf(m, __fmaf_ru(mx, unscale, kF16 ? -kProbExp : 0.f));
       if (__any_sync(kFull, mn != m)) {
         const float alpha = ex2(m - mn);
         l *= alpha;

@@ -83,6 +83,31 @@ def signs(seed):
 
 
 @pytest.mark.parametrize("fmt", ["int4", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(fmt, sign):
+    """Equal keys, so equal weights, whatever the score: its log2 is sign * 2^e for e from 10 to 100 in steps of 1 / 3.  Values whose
+    largest scale is a power of two (7 2^n) and others."""
+    mags = 2.0 ** (np.arange(10, 100, 1 / 3) / 2) / math.sqrt(128 / math.sqrt(128) * math.log2(math.e))
+    n, L, G = len(mags), 40, 4
+    k = torch.zeros(n, 1, L, 128, device="cuda")
+    q = torch.zeros(n, G, 128, device="cuda")
+    for i, a in enumerate(mags):
+        k[i, 0] = sign * float(a) * signs(i)
+        q[i] = float(a) * signs(i)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    v = torch.randint(-7, 8, (n, 1, L, 128), generator=g, device="cuda").float()
+    v[..., :8] = 7
+    v[1::2] *= 1.37
+    with Cache([L] * n, G, 1, fmt, 16, "f32", k=k, v=v) as c:
+        out = attend(c, q)
+        want = c.vr.double().mean(2)
+        bound = (2.0 ** -19 + 2.0 ** -20) * c.vr.double().abs().mean(2)
+        assert torch.isfinite(out).all()
+        assert ((out.double() - want).abs() <= bound).all()
+        check(c, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
 def test_rows_far_below_each_other(fmt):
     """One row takes all the weight: at the front, at the end, alone in its sequence; scores down to -1e37."""
     L, G = 70, 2
