@@ -21,9 +21,10 @@
 // Matrix mapping (mma.sync m16n8k16, float32 sums).  The 16 rows of the operand hold the group's heads more
 // than once, as a high part and residuals, so that no bits of queries and probabilities are lost:
 //   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
-//     to a maximum of 2^10 a head; probabilities are 2^11 times their value at most and value scales at most 2^4
-//     by the largest scale the warp has met (a power of two, moved like the running maximum), so
-//     float16's range holds both.  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
+//     to a maximum of 2^10 a head; probabilities are 2^14 times their value at most and value scales below 2
+//     by the largest scale the warp has met (a power of two, moved like the running maximum), so float16's
+//     range holds both, and the products that count keep 22 bits, while the scales met lie within 2^16 of each other.  Where
+//     they do not, the CTA takes its piece of the slice once more at the end, in float32 (attend_wide).  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
 //     are summed by themselves (starting at -8 times the sum of the queries, which centres
 //     the codes) and scaled once a (row, group), not once an element.
@@ -196,9 +197,13 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-constexpr float kProbExp = 11.f;         // 4 bits: probabilities are 2^11 times their value (less where scores' steps are coarser)
-constexpr float kScaleTop = 16.f;        // 4 bits: value scales in float16, at most this
-constexpr unsigned kScaleLow = 0x0d80u;  // bf16 2^-100: the least bound of the value scales
+// 4 bits: probabilities are 2^14 times their value (less where scores' steps are coarser), value scales in float16 below 2.  A
+// probability in two float16 parts is off by 2^-25 at most where its leading bits run out, against 2^14 of the row with the
+// largest: a row whose scale is 2^16 above that row's puts 2^-23 of the sum into it, and a scale that far down is exact.
+constexpr float kProbExp = 14.f;
+// In bf16 bits: the least and the largest bound of the value scales (2^-100, 2^126: their reciprocals are normal numbers), and
+// 2^8 and 2^16: scales from the bound down to 2^-8 of it need no look.
+constexpr unsigned kScaleLow = 0x0d80u, kScaleHigh = 0x7e80u, kScaleNear = 0x400u, kScaleSpan = 0x800u;
 
 // Rows of one slice: blocks [0, nb0) (sinks), blocks [b1, b1 + nb1) (window, or every block), then cnt listed rows.
 struct Slice {
@@ -243,10 +248,343 @@ constexpr unsigned kList = 0x10000u;
 constexpr int kQRow = 161;
 __device__ __forceinline__ int q_at(int d) { return d + 8 * (d >> 5); }
 
+// Queries of slice s: warp h takes head h of the group, a lane the pairs lane and lane + 32 (of dims that do not turn: neighbours).
+__device__ __forceinline__ void pair_at(const RopeTab128& tab, int j, int& d0, int& d1) {
+  const int half = tab.rot / 2;
+  d0 = j >= half ? tab.rot + 2 * (j - half) : tab.interleaved ? 2 * j : j;
+  d1 = j >= half || tab.interleaved ? d0 + 1 : d0 + half;
+}
+__device__ __forceinline__ float4 load_queries(const PagedAttendArgs& A, const RopeTab128& tab, int s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hkv = A.pool.Hkv;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (warp < A.G) {
+    const size_t at = ((size_t)(s / Hkv) * A.Hq + (size_t)(s % Hkv) * A.G + warp) * kHeadDim;
+    int a0, a1, b0, b1;
+    pair_at(tab, lane, a0, a1);
+    pair_at(tab, lane + 32, b0, b1);
+    if (A.q_f32) {
+      const float* q = static_cast<const float*>(A.q) + at;
+      x = make_float4(q[a0], q[a1], q[b0], q[b1]);
+    } else {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + at;
+      x = make_float4(__bfloat162float(q[a0]), __bfloat162float(q[a1]), __bfloat162float(q[b0]), __bfloat162float(q[b1]));
+    }
+  }
+  return x;
+}
+// To qs, rotated at position L - 1, times scale / ln 2.
+__device__ __forceinline__ void turn_queries(const PagedAttendArgs& A, const RopeTab128& tab, float4 x, float* qs, int L) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= A.G) return;
+  float* const q = qs + warp * kQRow;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    int d0, d1;
+    pair_at(tab, j, d0, d1);
+    const float q0 = i ? x.z : x.x, q1 = i ? x.w : x.y;
+    float c = 1.f, sn = 0.f;
+    if (j < tab.rot / 2) rope_cs(tab.f_pi[j], (double)(L - 1), (float)tab.mag, c, sn);
+    q[q_at(d0)] = (q0 * c - q1 * sn) * A.scale_log2;
+    q[q_at(d1)] = (q0 * sn + q1 * c) * A.scale_log2;
+  }
+}
+
+// The warps' states in mbuf to the output, or to the CTA's state and, from the last of the slice's CTAs c0 .. c1, to the output.
+template <int W, bool kF16>
+__device__ __forceinline__ void finish(const PagedAttendArgs& A, const float* mbuf, int* s_merge, int s, int c0, int c1) {
+  constexpr int kBoxes = (W + 1) / 2;
+  const int tid = threadIdx.x, G = A.G;
+  const int b = s / A.pool.Hkv;
+  const size_t h0 = (size_t)b * A.Hq + (size_t)(s - b * A.pool.Hkv) * G;
+  const int xl = tid & 31, xh = xl >> 2;   // thread x: lane xl's sums of column tiles 2 (x / 32) and the next; its head
+  const bool takes = tid < 256 && xh < G;
+  float4* const part = reinterpret_cast<float4*>(A.part);
+  constexpr int kState = kMergeWords / 4;
+  // normalised sums of 4, to the output
+  auto put = [&](float4 v, float M, float Ls) {
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;   // no weight at all: zeros
+    const int k2 = 2 * (tid >> 5);                  // column tile
+    float* const to = A.out + (h0 + xh) * kHeadDim;
+    // (tile nt, e) is dim 32 t4 + 16 e + nt in 4 bits, 8 nt + 2 t4 + e in bf16
+    if (kF16) {
+      float2* const at = reinterpret_cast<float2*>(to + 32 * (xl & 3) + k2);
+      at[0] = make_float2(v.x * inv, v.z * inv);
+      at[8] = make_float2(v.y * inv, v.w * inv);
+    } else {
+      float2* const at = reinterpret_cast<float2*>(to + 8 * k2 + 2 * (xl & 3));
+      at[0] = make_float2(v.x * inv, v.y * inv);
+      at[4] = make_float2(v.z * inv, v.w * inv);
+    }
+    if (A.lse && tid < 32 && (xl & 3) == 0) A.lse[h0 + xh] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
+  };
+  if (takes) {
+    float M = kNoMax, Ls = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float2 ml[kBoxes];
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) {
+      ml[i] = *reinterpret_cast<const float2*>(mbuf + (size_t)i * kMergeWords + 1024 + 4 * xl);
+      M = fmaxf(M, ml[i].x);
+    }
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) {
+      const float w = exp2f(ml[i].x - M);
+      const float4 v = *reinterpret_cast<const float4*>(mbuf + (size_t)i * kMergeWords + 4 * tid);
+      Ls += ml[i].y * w;
+      num.x += v.x * w;
+      num.y += v.y * w;
+      num.z += v.z * w;
+      num.w += v.w * w;
+    }
+    if (c0 == c1) {
+      put(num, M, Ls);
+    } else {
+      float4* const to = part + (size_t)(blockIdx.x + s) * kState;
+      to[tid] = num;
+      if (tid < 32) to[256 + xl] = make_float4(M, Ls, 0.f, 0.f);
+      __threadfence();
+    }
+  }
+  if (c0 == c1) return;
+  // ---- the last CTA of the slice merges the CTAs' states in order
+  __syncthreads();
+  if (tid == 0) *s_merge = atomicAdd(&A.ticket[s], 1u) == (unsigned)(c1 - c0);
+  __syncthreads();
+  if (!*s_merge) return;
+  __threadfence();
+  if (takes) {
+    float M = kNoMax, Ls = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kB = 8;
+    for (int c = c0; c <= c1; c += kB) {
+      float4 v[kB], ml[kB];
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const float4* from = part + (size_t)(min(c + i, c1) + s) * kState;
+        v[i] = __ldcg(from + tid);
+        ml[i] = __ldcg(from + 256 + xl);
+      }
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        if (c + i > c1) break;
+        const float mn = fmaxf(M, ml[i].x), sa = exp2f(M - mn), sb = exp2f(ml[i].x - mn);
+        Ls = Ls * sa + ml[i].y * sb;
+        num.x = num.x * sa + v[i].x * sb;
+        num.y = num.y * sa + v[i].y * sb;
+        num.z = num.z * sa + v[i].z * sb;
+        num.w = num.w * sa + v[i].w * sb;
+        M = mn;
+      }
+    }
+    put(num, M, Ls);
+  }
+  if (tid == 0) A.ticket[s] = 0u;   // ready for the next call
+}
+
+// 4-bit word to 8 values n - 8 (exact small integers).
+__device__ __forceinline__ void centred(unsigned w, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x4b000000u | (w >> (4 * i) & 15u)) - 8388616.f;
+}
+// A CTA's piece of a slice of 4-bit pages in float32 throughout, for rows whose value scales are too far apart for float16 products.  The
+// queries are in qs; `unit` is the piece's first unit of the slice, `items` the number of its items, which the warps take in turn.  A lane
+// scores one row of an item for every head, then sums 4 dims over the rows.  Leaves the states in mbuf as the kernel's own
+// hand-over does.  One row of 1M, 8 KV heads of 8 queries: 2.2 ms in place of 0.37 (one CTA takes 57000 rows again); of 64K, 170 us
+// in place of 50.  Loads of queries and shuffles bound it.
+template <int W, int U>
+__device__ __forceinline__ void attend_wide(const PagedAttendArgs& A, const Slice& S, const float* qs, float* mbuf, int s, int unit, int items) {
+  static_assert(U == 2, "a lane a row of an item");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = A.G;
+  const int b = s / A.pool.Hkv, g = s - b * A.pool.Hkv;
+  // queries as [8][128], for 16-byte loads; zeros for heads that the group does not have
+  for (int i = threadIdx.x; i < kMaxGroup * kHeadDim; i += W * 32)
+    mbuf[i] = i / kHeadDim < G ? qs[i / kHeadDim * kQRow + q_at(i % kHeadDim)] : 0.f;
+  __syncthreads();
+  const float4* const q4 = reinterpret_cast<const float4*>(mbuf);
+  float m[kMaxGroup], l[kMaxGroup], acc[kMaxGroup][4];
+#pragma unroll
+  for (int h = 0; h < kMaxGroup; ++h) {
+    m[h] = kNoMax;
+    l[h] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[h][c] = 0.f;
+  }
+#pragma unroll 1
+  for (int k = warp; k < items; k += W) {
+    // ---- the lane's row: byte offset of its block, plus its place; -1: not attended
+    const int u = unit + k * U + lane / 16, r16 = lane & 15;
+    int pos = -1;
+    if (u < S.nb0 + S.nb1) {
+      const int at = (u < S.nb0 ? u : S.b1 + (u - S.nb0)) * kBlockTok + r16;
+      if (at < S.L && (at < S.n_s || at >= S.w_lo)) pos = at;
+    } else if ((u - S.nb0 - S.nb1) * 16 + r16 < S.cnt) {
+      pos = __ldg(A.list + (long long)s * A.list_stride + (u - S.nb0 - S.nb1) * 16 + r16);
+      if (pos >= S.L) pos = -1;
+    }
+    long long row = -1;
+    if (pos >= 0) {
+      const unsigned blk = (unsigned)pos / kBlockTok, pg = blk / (unsigned)A.pool.page_blocks;
+      const int id = __ldg(A.pool.table + (size_t)b * A.pool.max_pages + pg);
+      if ((unsigned)id < (unsigned)A.pool.n_pages)
+        row = ((long long)id * A.pool.Hkv + g) * A.pool.head_bytes + (long long)(blk - pg * A.pool.page_blocks) * kBlockBytes4 +
+              pos % kBlockTok;
+    }
+    // ---- its scores
+    float p[kMaxGroup];
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h) p[h] = row >= 0 ? 0.f : -INFINITY;
+    if (row >= 0) {
+      const int r = (int)(row & 15);
+      const unsigned char* const blk = A.pool.pages + (row - r);
+      const uint2 sc = __ldg(reinterpret_cast<const uint2*>(blk + 2 * kBlockTok * kRow4 + r * 16));
+      const float ks[4] = {bf16_lo(sc.x), bf16_hi(sc.x), bf16_lo(sc.y), bf16_hi(sc.y)};
+#pragma unroll 1
+      for (int w4 = 0; w4 < 4; ++w4) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(blk + r * kRow4) + w4);
+        const uint32_t code[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          float f[8];
+          centred(code[gr], f);
+#pragma unroll
+          for (int h = 0; h < kMaxGroup; ++h) {
+            const float4 x = q4[32 * h + 8 * w4 + 2 * gr], y = q4[32 * h + 8 * w4 + 2 * gr + 1];
+            float d = x.x * f[0];
+            d = fmaf(x.y, f[1], d);
+            d = fmaf(x.z, f[2], d);
+            d = fmaf(x.w, f[3], d);
+            d = fmaf(y.x, f[4], d);
+            d = fmaf(y.y, f[5], d);
+            d = fmaf(y.z, f[6], d);
+            d = fmaf(y.w, f[7], d);
+            p[h] = fmaf(ks[gr], d, p[h]);
+          }
+        }
+      }
+    }
+    // ---- probabilities
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h) {
+      float mx = p[h];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      const float mn = fmaxf(m[h], mx), alpha = exp2f(m[h] - mn);
+      m[h] = mn;
+      p[h] = exp2f(p[h] - mn);
+      l[h] = fmaf(l[h], alpha, p[h]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[h][c] *= alpha;
+    }
+    // ---- sums of dims 4 lane .. 4 lane + 3, of value scale group lane % 4; 8 rows' loads under way together
+    constexpr int kRows = 8;
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32; j0 += kRows) {
+      unsigned w[kRows];
+      float y[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const long long at = __shfl_sync(kFull, row, j0 + j);
+        const int r = at < 0 ? 0 : (int)(at & 15);
+        const unsigned char* const blk = A.pool.pages + (at < 0 ? 0 : at - r);
+        w[j] = __ldg(reinterpret_cast<const unsigned short*>(blk + kBlockTok * kRow4 + r * kRow4) + lane);
+        const unsigned vs = __ldg(reinterpret_cast<const unsigned short*>(blk + 2 * kBlockTok * kRow4 + r * 16 + 8) + (lane & 3));
+        y[j] = at < 0 ? 0.f : __uint_as_float(vs << 16);
+      }
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = y[j] * (__uint_as_float(0x4b000000u | (w[j] >> (4 * c) & 15u)) - 8388616.f);
+#pragma unroll
+        for (int h = 0; h < kMaxGroup; ++h) {
+          const float x = __shfl_sync(kFull, p[h], j0 + j);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[h][c] = fmaf(x, v[c], acc[h][c]);
+        }
+      }
+    }
+  }
+  // ---- the upper half of the warps first, the lower adds its own: dim d = 32 t + 16 e + n of head h at [n / 2][4 h + t][2 (n % 2) + e]
+  constexpr int kBoxes = (W + 1) / 2;
+  float* const box = mbuf + (size_t)(warp % kBoxes) * kMergeWords;
+#pragma unroll 1
+  for (int half = 1; half >= 0; --half) {
+    __syncthreads();
+    if (warp / kBoxes == half) {
+      const bool other = half == 0 && warp + kBoxes < W;
+#pragma unroll
+      for (int h = 0; h < kMaxGroup; ++h) {
+        float ls = l[h];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(kFull, ls, o);
+        float* const ml = box + 1024 + 16 * h;
+        const float m2 = other ? ml[0] : kNoMax, l2 = other ? ml[1] : 0.f;
+        const float mn = fmaxf(m[h], m2), sa = exp2f(m[h] - mn), sb = exp2f(m2 - mn);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int d = 4 * lane + c, n = d & 15;
+          float* const x = box + 4 * (32 * (n >> 1) + 4 * h + (d >> 5)) + 2 * (n & 1) + (d >> 4 & 1);
+          *x = acc[h][c] * sa + (other ? *x * sb : 0.f);
+        }
+        __syncwarp();
+        if (lane < 4) {
+          ml[4 * lane] = mn;
+          ml[4 * lane + 1] = ls * sa + l2 * sb;
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The CTAs that share slice s, whose items are [lo, hi).  split: see s_split.
+__device__ __forceinline__ void owners(const int4& split, int nb, long long T, long long lo, long long hi, int& c0, int& c1) {
+  const bool aligned = split.z >= 0;
+  c0 = aligned ? split.y : (int)(((lo + 1) * nb - 1) / T);
+  c1 = aligned ? split.y + split.z - 1 : (int)((hi * nb - 1) / T);
+}
+// The pieces marked in redo, once more in float32.  Finds everything out again from shared memory: handed over, the
+// CTA's share alone cost 1M rows 18 us.
+template <int W, int U, int S>
+__device__ __noinline__ void redo_wide(const PagedAttendArgs& A, const RopeTab128& tab, const unsigned* redo, const int4* s_split, int* s_merge) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* const mbuf = reinterpret_cast<float*>(smem + (size_t)W * S * U * kBlockBytes4);
+  float* const qs = mbuf + (W + 1) / 2 * kMergeWords;
+  const long long* const rpre = reinterpret_cast<const long long*>(qs + kMaxGroup * kQRow);
+  const int2* const sinfo = reinterpret_cast<const int2*>(rpre + A.n_slices + 1);
+  const int NS = A.n_slices;
+  bool big = NS > (int)gridDim.x;
+  for (int s = threadIdx.x; s < NS; s += W * 32) big = big || rpre[s + 1] - rpre[s] > 2 * W;
+  const bool small = !__syncthreads_or(big);
+  const int4 split = small ? make_int4(blockIdx.x, blockIdx.x, 1, 0) : *s_split;
+  const long long T = rpre[NS];
+  const int nb = (long long)gridDim.x < T ? (int)gridDim.x : (int)T;
+  for (int s = 0; s < NS; ++s) {
+    if (!(redo[s >> 5] >> (s & 31) & 1u)) continue;
+    __syncthreads();
+    turn_queries(A, tab, load_queries(A, tab, s), qs, sinfo[s].x);
+    __syncthreads();
+    long long lo = rpre[s], hi = rpre[s + 1];
+    if (split.z >= 0) {
+      const long long n = hi - lo;
+      hi = lo + (blockIdx.x - split.y + 1) * n / split.z;
+      lo = lo + (blockIdx.x - split.y) * n / split.z;
+    } else {
+      lo = max(lo, (long long)blockIdx.x * T / nb);
+      hi = min(hi, (long long)(blockIdx.x + 1) * T / nb);
+    }
+    attend_wide<W, U>(A, make_slice(A, s % A.pool.Hkv, sinfo[s].x, sinfo[s].y), qs, mbuf, s, (int)(lo - rpre[s]) * U, (int)(hi - lo));
+    int c0, c1;
+    owners(split, nb, T, rpre[s], rpre[s + 1], c0, c1);
+    finish<W, true>(A, mbuf, s_merge, s, c0, c1);
+  }
+}
+
 // W warps, items of U units (4 bits 2, bf16 1), S ring slots a warp; WIDE: more than 4 heads a group (bf16 only, see the matrix mapping); LISTED: a
 // selection is given.
 template <int FMT, int W, int U, int S, bool WIDE, bool LISTED>
-__global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArgs A, const __grid_constant__ RopeTab128 tab) {
+__global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const __grid_constant__ PagedAttendArgs A, const __grid_constant__ RopeTab128 tab) {
   constexpr bool kF16 = FMT == kPageInt4;
   constexpr int kBlk = FMT == kPageInt4 ? kBlockBytes4 : kBlockBytes16;
   constexpr int kItems = 32 / U;   // items that 32 lanes look up
@@ -267,6 +605,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   __shared__ uint4 qf[kF16 ? 8 * 32 : 1];      // 4 bits: query operands, a lane's 16 bytes of each k-step
   __shared__ float2 q8[kF16 ? 4 * 8 : 1];      // 4 bits: -8 times a scale group's sum of queries (high, residual), each head
   __shared__ __align__(16) float kscale[kF16 ? 4 * W * 32 : 4];   // 4 bits, of the item in hand: scales of K, by group and row
+  __shared__ int s_wide, any_redo;             // 4 bits: the piece in hand has to be taken again; some piece has
+  __shared__ unsigned redo[kF16 ? kMaxPagedSlices / 32 : 1];   // 4 bits: a bit for each slice of such a piece
   __shared__ uint4 vscale[kF16 ? W * 16 : 1];  // and of V in float16, (row, row + 1) pairs of each group
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,6 +618,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   if (kF16) {   // heads that the group does not have
     if (tid < 256) qf[kF16 ? tid : 0] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 32) q8[kF16 ? tid : 0] = make_float2(0.f, 0.f);
+    if (tid < kMaxPagedSlices / 32) redo[kF16 ? tid : 0] = 0u;
+    if (tid == 0) s_wide = any_redo = 0;
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
@@ -430,7 +772,6 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
     r_lo = (long long)blockIdx.x * T / nb;
     r_hi = (long long)(blockIdx.x + 1) * T / nb;
   }
-  auto owner = [&](long long r) { return (int)(((r + 1) * nb - 1) / T); };
   auto slice_of = [&](long long r) {
     int lo = 0, hi = NS - 1;
     while (lo < hi) {
@@ -442,29 +783,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   };
   const int s_first = aligned ? split.x : slice_of(r_lo), s_last = aligned ? split.x : slice_of(r_hi - 1);
 
-  // ---- a slice's queries: warp h takes head h of the group, a lane the pairs lane and lane + 32
-  const int half = tab.rot / 2;
-  auto pair_at = [&](int j, int& d0, int& d1) {
-    d0 = j >= half ? tab.rot + 2 * (j - half) : tab.interleaved ? 2 * j : j;
-    d1 = j >= half || tab.interleaved ? d0 + 1 : d0 + half;
-  };
-  auto load_q = [&](int s) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (warp < G) {
-      const size_t at = ((size_t)(s / Hkv) * A.Hq + (size_t)(s % Hkv) * G + warp) * kHeadDim;
-      int a0, a1, b0, b1;
-      pair_at(lane, a0, a1);
-      pair_at(lane + 32, b0, b1);
-      if (A.q_f32) {
-        const float* q = static_cast<const float*>(A.q) + at;
-        x = make_float4(q[a0], q[a1], q[b0], q[b1]);
-      } else {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + at;
-        x = make_float4(__bfloat162float(q[a0]), __bfloat162float(q[a1]), __bfloat162float(q[b0]), __bfloat162float(q[b1]));
-      }
-    }
-    return x;
-  };
+  auto load_q = [&](int s) { return load_queries(A, tab, s); };
   float4 q_next = load_q(s_first);
   const uint32_t ring_a = smem_u32(ring) + warp * S * U * kBlk, bar_a = smem_u32(&full[warp * S]);
   const uint64_t pol = l2_evict_first();
@@ -632,22 +951,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
   for (int s = s_first; s <= s_last; ++s) {
     if (rpre[s + 1] == rpre[s]) continue;
     const int i_end = (int)(min(r_hi, rpre[s + 1]) - r_lo);
-    const int b = s / Hkv, g = s - b * Hkv;
-    const size_t h0 = (size_t)b * A.Hq + (size_t)g * G;
     // ---- the group's queries, rotated at position L - 1, times scale / ln 2
+    turn_queries(A, tab, q_next, qs, sinfo[s].x);
     if (warp < G) {
       float* const q = qs + warp * kQRow;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = lane + 32 * i;
-        int d0, d1;
-        pair_at(j, d0, d1);
-        const float q0 = i ? q_next.z : q_next.x, q1 = i ? q_next.w : q_next.y;
-        float c = 1.f, sn = 0.f;
-        if (j < half) rope_cs(tab.f_pi[j], (double)(sinfo[s].x - 1), (float)tab.mag, c, sn);
-        q[q_at(d0)] = (q0 * c - q1 * sn) * A.scale_log2;
-        q[q_at(d1)] = (q0 * sn + q1 * c) * A.scale_log2;
-      }
       if (kF16) {
         __syncwarp();
         // dim lane + 32 t of scale group lane / 8: k-step 2 (lane / 8) + i holds dims 32 t + 8 (lane / 8) + 2 i + {0, 4, 1, 5}
@@ -708,8 +1015,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       }
     }
     float m = kNoMax, l = 0.f;
-    unsigned vlim = kScaleLow;                                        // 4 bits: bound of the value scales met (bf16 bits)
-    float vmul = kScaleTop * __uint_as_float((254u << 23) - (kScaleLow << 16));   // kScaleTop / bound
+    // 4 bits: bound of the value scales met, a power of two in bf16 bits, with the number of binades below it that they reach (zeros
+    // aside) in its low bits; and the inverse of the bound.  (A variable of its own for the binades cost 1M rows 10 us.)
+    unsigned vlim = 0u;
+    float vmul = __uint_as_float((254u << 23) - (kScaleLow << 16));
     // Sums over the rows, of column tile nt.  An item's products are summed apart and added by rounded additions: the
     // tensor cores truncate what they add to, and over the hundreds of items of a long context that
     // pulls sums towards zero (4e-6 at 1M rows).  High and residual rows meet here, so it is half the registers.
@@ -744,24 +1053,29 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       if (kF16) {
         uint4 w = *reinterpret_cast<const uint4*>(st + lane / 16 * kBlk + 2 * kBlockTok * kRow4 + (lane & 15) * 16);
         if (part && !((lane < 16 ? vm[0] : vm[U - 1]) >> (lane & 15) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t vtop = max_u16x2(w.z, w.w);
-        vtop = max(vtop & 0xffffu, vtop >> 16);
-        if (__any_sync(kFull, vtop > vlim)) {
-          if (vtop >= 0x7f80u) {   // a NaN scale: the finite ones decide
-            auto finite = [](uint32_t x) { return x < 0x7f80u ? x : 0u; };
-            vtop = max(max(finite(w.z & 0xffffu), finite(w.z >> 16)), max(finite(w.w & 0xffffu), finite(w.w >> 16)));
-          }
+        // any of the four outside (vlim - kScaleNear, vlim] (a borrow comes from one outside)
+        if (__any_sync(kFull, max_u16x2(vlim * 0x10001u - w.z, vlim * 0x10001u - w.w) & (0x10000u - kScaleNear) * 0x10001u)) {
+          auto finite = [](uint32_t x) { return x < 0x7f80u ? x : 0u; };           // NaN: the finite ones decide,
+          auto some = [](uint32_t x) { return x - 1u < 0x7f7fu ? x : 0x7f80u; };   // and those that are not 0
+          unsigned vtop = max(max(finite(w.z & 0xffffu), finite(w.z >> 16)), max(finite(w.w & 0xffffu), finite(w.w >> 16)));
+          unsigned vmin = min(min(some(w.z & 0xffffu), some(w.z >> 16)), min(some(w.w & 0xffffu), some(w.w >> 16)));
           vtop = __reduce_max_sync(kFull, vtop);
-          if (vtop > vlim) {   // the power of two at or above it (2^126 at most: its reciprocal is a normal number)
-            vlim = min((vtop + 0x7fu) & 0x7f80u, 0x7e80u);
-            const float now = kScaleTop * __uint_as_float((254u << 23) - (vlim << 16)), by = now / vmul;
+          vmin = __reduce_min_sync(kFull, vmin) & 0x7f80u;
+          unsigned lim = vlim & 0x7f80u, low = vlim ? min(vmin, lim - (vlim & 0x7fu) * 0x80u) : vmin;
+          if (vtop > lim) {   // the power of two at or above it
+            lim = min(max((vtop + 0x7fu) & 0x7f80u, kScaleLow), kScaleHigh);
+            const float now = __uint_as_float((254u << 23) - (lim << 16)), by = now / vmul;
             vmul = now;
 #pragma unroll
             for (int nt = 0; nt < 16; ++nt) {
               acc[nt][0] *= by;
               acc[nt][1] *= by;
             }
+            low = min(low, lim - kScaleNear);   // rows that are not looked at
           }
+          const unsigned span = min(lim - min(low, lim), kScaleSpan + 0x80u) >> 7;
+          if (span > kScaleSpan >> 7) s_wide = 1;
+          vlim = lim | span;
         }
         kscale[128 * warp + lane] = bf16_lo(w.x);
         kscale[128 * warp + 32 + lane] = bf16_hi(w.x);
@@ -849,7 +1163,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
         for (int j = 0; j < 2; ++j) mx = fmaxf(mx, fmaxf(p[u][j][0], p[u][j][1]));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      // rounded up: where 11 is less than a step of the score, a rounding down would let the top probability past 2^11
+      // rounded up: where 14 is less than a step of the score, a rounding down would let the top probability past 2^14
       const float mn = fmaxf(m, __fmaf_ru(mx, unscale, kF16 ? -kProbExp : 0.f));
       if (__any_sync(kFull, mn != m)) {
         const float alpha = ex2(m - mn);
@@ -881,7 +1195,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
           for (int j = 0; j < 2; ++j) {
             const unsigned char* vb = st + u * kBlk + kBlockTok * kRow4 + gid * 8;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) vw[u][j][e] = *reinterpret_cast<const uint2*>(vb + (8 * j + 2 * t4 + e) * kRow4);
+            for (int e = 0; e < 2; ++e) {   // a word here, the other as late as it may be (one load of both: 1M rows 357 us in place of 345)
+              vw[u][j][e].x = *reinterpret_cast<const volatile uint32_t*>(vb + (8 * j + 2 * t4 + e) * kRow4);
+              vw[u][j][e].y = *reinterpret_cast<const uint32_t*>(vb + (8 * j + 2 * t4 + e) * kRow4 + 4);
+            }
             split_f16(p[u][j][0], p[u][j][1], ph[u][j], pl[u][j]);
             sv[u][j] = vscale[16 * warp + 8 * u + 4 * j + t4];
           }
@@ -1001,91 +1318,23 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const PagedAttendArg
       }
       hand_over();
     }
+    const bool wide = kF16 && s_wide;   // its result is left for redo_wide
     __syncthreads();
-    const int c0 = aligned ? split.y : owner(rpre[s]), c1 = aligned ? split.y + split.z - 1 : owner(rpre[s + 1] - 1);
-    const int xl = tid & 31, xh = xl >> 2;   // thread x: lane xl's sums of column tiles 2 (x / 32) and the next; its head
-    const bool takes = tid < 256 && xh < G;
-    float4* const part = reinterpret_cast<float4*>(A.part);
-    constexpr int kState = kMergeWords / 4;
-    // normalised sums of 4, to the output
-    auto put = [&](float4 v, float M, float Ls) {
-      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;   // no weight at all: zeros
-      const int k2 = 2 * (tid >> 5);                  // column tile
-      float* const to = A.out + (h0 + xh) * kHeadDim;
-      // (tile nt, e) is dim 32 t4 + 16 e + nt in 4 bits, 8 nt + 2 t4 + e in bf16
-      if (kF16) {
-        float2* const at = reinterpret_cast<float2*>(to + 32 * (xl & 3) + k2);
-        at[0] = make_float2(v.x * inv, v.z * inv);
-        at[8] = make_float2(v.y * inv, v.w * inv);
-      } else {
-        float2* const at = reinterpret_cast<float2*>(to + 8 * k2 + 2 * (xl & 3));
-        at[0] = make_float2(v.x * inv, v.y * inv);
-        at[4] = make_float2(v.z * inv, v.w * inv);
+    if (wide) {
+      if (tid == 0) {
+        s_wide = 0;
+        any_redo = 1;
+        redo[kF16 ? s >> 5 : 0] |= 1u << (s & 31);
       }
-      if (A.lse && tid < 32 && (xl & 3) == 0) A.lse[h0 + xh] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
-    };
-    if (takes) {
-      float M = kNoMax, Ls = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      float2 ml[kBoxes];
-#pragma unroll
-      for (int i = 0; i < kBoxes; ++i) {
-        ml[i] = *reinterpret_cast<const float2*>(mbuf + (size_t)i * kMergeWords + 1024 + 4 * xl);
-        M = fmaxf(M, ml[i].x);
-      }
-#pragma unroll
-      for (int i = 0; i < kBoxes; ++i) {
-        const float w = exp2f(ml[i].x - M);
-        const float4 v = *reinterpret_cast<const float4*>(mbuf + (size_t)i * kMergeWords + 4 * tid);
-        Ls += ml[i].y * w;
-        num.x += v.x * w;
-        num.y += v.y * w;
-        num.z += v.z * w;
-        num.w += v.w * w;
-      }
-      if (c0 == c1) {
-        put(num, M, Ls);
-      } else {
-        float4* const to = part + (size_t)(blockIdx.x + s) * kState;
-        to[tid] = num;
-        if (tid < 32) to[256 + xl] = make_float4(M, Ls, 0.f, 0.f);
-        __threadfence();
-      }
+      __syncthreads();
+      continue;
     }
-    if (c0 == c1) continue;
-    // ---- the last CTA of the slice merges the CTAs' states in order
-    __syncthreads();
-    if (tid == 0) s_merge = atomicAdd(&A.ticket[s], 1u) == (unsigned)(c1 - c0);
-    __syncthreads();
-    if (!s_merge) continue;
-    __threadfence();
-    if (takes) {
-      float M = kNoMax, Ls = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kB = 8;
-      for (int c = c0; c <= c1; c += kB) {
-        float4 v[kB], ml[kB];
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          const float4* from = part + (size_t)(min(c + i, c1) + s) * kState;
-          v[i] = __ldcg(from + tid);
-          ml[i] = __ldcg(from + 256 + xl);
-        }
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          if (c + i > c1) break;
-          const float mn = fmaxf(M, ml[i].x), sa = exp2f(M - mn), sb = exp2f(ml[i].x - mn);
-          Ls = Ls * sa + ml[i].y * sb;
-          num.x = num.x * sa + v[i].x * sb;
-          num.y = num.y * sa + v[i].y * sb;
-          num.z = num.z * sa + v[i].z * sb;
-          num.w = num.w * sa + v[i].w * sb;
-          M = mn;
-        }
-      }
-      put(num, M, Ls);
-    }
-    if (tid == 0) A.ticket[s] = 0u;   // ready for the next call
+    int c0, c1;
+    owners(split, nb, T, rpre[s], rpre[s + 1], c0, c1);
+    finish<W, kF16>(A, mbuf, &s_merge, s, c0, c1);
+  }
+  if constexpr (kF16) {   // any_redo is set before a barrier
+    if (any_redo) redo_wide<W, U, S>(A, tab, redo, &s_split, &s_merge);
   }
 }
 

@@ -136,3 +136,51 @@ def unit_cache(seed, n, Hkv, L, fmt, lens=None, change=None):
     if change:
         change(q, k, v)
     return q, Cache(lens or [L] * n, 4 * Hkv, Hkv, fmt, 16, "f32", k=k, v=v)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+@pytest.mark.parametrize("gap", [0, 12, 30, 90])
+@pytest.mark.parametrize("at", [0, 57, 899])
+def test_one_row_of_larger_values(fmt, gap, at):
+    """A row whose values are 2^k times the others', its score about `gap` below them: it has no weight, all of it, or some."""
+    ks = [0, 8, 12, 14, 18, 20, 22, 26, 30, 45, 60, 90]
+
+    def change(q, k, v):
+        q[:] = q[:, :1]     # one direction, so that the row is low for every head
+        for i, e in enumerate(ks):
+            v[i, :, at] *= 2.0 ** e
+            u = q[i, 0] / q[i, 0].norm()
+            k[i, 0, at] = -u * gap * math.sqrt(128) / float(q[i, 0].norm())
+    q, c = unit_cache(5, len(ks), 1, 900, fmt, change=change)
+    with c:
+        check(c, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+@pytest.mark.parametrize("e", [12, 20, 30, 70, -30, -70])
+def test_one_group_of_larger_values(fmt, e):
+    """One channel 2^e times the rest: the groups of dims have their own scales, and keep their own precision."""
+    def change(q, k, v):
+        v[0, :, :, 37] *= 2.0 ** e
+        v[1] *= 2.0 ** e
+        v[1, :, ::2] = v[1, :, ::2] * 2.0 ** -e
+        v[2, :, :500] *= 2.0 ** e
+    q, c = unit_cache(6, 3, 2, 1000, fmt, change=change)
+    with c:
+        check(c, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_values_that_grow_as_their_weights_fall(fmt):
+    """Weights and values that make up for each other: every row counts alike."""
+    def change(q, k, v):
+        q[:] = q[:, :1]
+        for i in range(2):
+            u = q[i, 0] / q[i, 0].norm()
+            x = torch.linspace(0, 60, 800, device="cuda")
+            k[i, 0] = -u * x[:, None] * math.sqrt(128) * math.log(2) / q[i, 0].norm()
+            v[i, 0] *= torch.exp2(x)[:, None]
+        k[1], v[1] = k[1].flip(1), v[1].flip(1)
+    q, c = unit_cache(7, 2, 1, 800, fmt, change=change)
+    with c:
+        check(c, q, fmt)
