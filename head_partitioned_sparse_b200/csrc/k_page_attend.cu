@@ -201,9 +201,9 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 // probability in two float16 parts is off by 2^-25 at most where its leading bits run out, against 2^14 of the row with the
 // largest: a row whose scale is 2^16 above that row's puts 2^-23 of the sum into it, and a scale that far down is exact.
 constexpr float kProbExp = 14.f;
-// In bf16 bits: the least and the largest bound of the value scales (2^-100, 2^126: their reciprocals are normal numbers), and
-// 2^8 and 2^16: scales from the bound down to 2^-8 of it need no look.
-constexpr unsigned kScaleLow = 0x0d80u, kScaleHigh = 0x7e80u, kScaleNear = 0x400u, kScaleSpan = 0x800u;
+// In bf16 bits: the least and the largest bound of the value scales (2^-100, 2^80: 2^14 times the sum of 2^24 rows stays
+// in float32; what has larger ones is taken in float32, too), and 2^8 and 2^16: scales from the bound down to 2^-8 of it need no look.
+constexpr unsigned kScaleLow = 0x0d80u, kScaleHigh = 0x6780u, kScaleNear = 0x400u, kScaleSpan = 0x800u;
 
 // Rows of one slice: blocks [0, nb0) (sinks), blocks [b1, b1 + nb1) (window, or every block), then cnt listed rows.
 struct Slice {
@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const __grid_constan
             low = min(low, lim - kScaleNear);   // rows that are not looked at
           }
           const unsigned span = min(lim - min(low, lim), kScaleSpan + 0x80u) >> 7;
-          if (span > kScaleSpan >> 7) s_wide = 1;
+          if (span > kScaleSpan >> 7 || vtop > kScaleHigh) s_wide = 1;
           vlim = lim | span;
         }
         kscale[128 * warp + lane] = bf16_lo(w.x);

@@ -184,3 +184,17 @@ def test_values_that_grow_as_their_weights_fall(fmt):
     q, c = unit_cache(7, 2, 1, 800, fmt, change=change)
     with c:
         check(c, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_values_near_the_end_of_float32(fmt):
+    """Values up to 2^123 with groups and rows of zeros beside them; the sum of a row's weights times its values stays
+    within float32."""
+    def change(q, k, v):
+        v[0, :, :, 32:] = 0
+        v[0, :, 3:] = 0
+        v *= 2.0 ** 121 / v.abs().amax()
+    q, c = unit_cache(8, 2, 1, 20, fmt, change=change)
+    with c:
+        out, _ = check(c, q, fmt)
+        assert torch.isfinite(out).all()
