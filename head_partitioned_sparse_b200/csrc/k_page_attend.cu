@@ -21,10 +21,10 @@
 // Matrix mapping (mma.sync m16n8k16, float32 sums).  The 16 rows of the operand hold the group's heads more
 // than once, as a high part and residuals, so that no bits of queries and probabilities are lost:
 //   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
-//     to a maximum of 2^10 a head; probabilities are 2^14 times their value at most and value scales below 2
+//     to a maximum of 2^14 a head (the largest of every scale group then keeps 22 bits down to 2^-13 of that); probabilities are 2^14 times their value at most and value scales below 2
 //     by the largest scale the warp has met (a power of two, moved like the running maximum), so float16's
 //     range holds both, and the products that count keep 22 bits, while the scales met lie within 2^16 of each other.  Where
-//     they do not, the CTA takes its piece of the slice once more at the end, in float32 (attend_wide).  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
+//     scales or queries lie farther apart, the CTA takes its piece of the slice once more at the end, in float32 (attend_wide).  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
 //     are summed by themselves (starting at -8 times the sum of the queries, which centres
 //     the codes) and scaled once a (row, group), not once an element.
@@ -387,7 +387,8 @@ __device__ __forceinline__ void centred(unsigned w, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x4b000000u | (w >> (4 * i) & 15u)) - 8388616.f;
 }
-// A CTA's piece of a slice of 4-bit pages in float32 throughout, for rows whose value scales are too far apart for float16 products.  The
+// A CTA's piece of a slice of 4-bit pages in float32 throughout, for rows whose value scales, or queries whose scale groups, are too far apart
+// for float16 products.  The
 // queries are in qs; `unit` is the piece's first unit of the slice, `items` the number of its items, which the warps take in turn.  A lane
 // scores one row of an item for every head, then sums 4 dims over the rows.  Leaves the states in mbuf as the kernel's own
 // hand-over does.  One row of 1M, 8 KV heads of 8 queries: 2.2 ms in place of 0.37 (one CTA takes 57000 rows again); of 64K, 170 us
@@ -964,11 +965,15 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const __grid_constan
           x[t] = q[q_at(lane + 32 * t)];
           top = fmaxf(top, fabsf(x[t]));
         }
+        float part = top;   // of the scale group
+#pragma unroll
+        for (int o = 1; o <= 4; o <<= 1) part = fmaxf(part, __shfl_xor_sync(kFull, part, o));
         top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
-        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -116), 112);
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 112);
+        if (part > 0.f && part < top * 0x1p-13f) s_wide = 1;
         const bool odd = lane & 1;   // the operand's second half, whose codes count 16 times
-        const float f = __uint_as_float((unsigned)(127 + 10 - e) << 23) * (odd ? 0.0625f : 1.f);
-        if (lane == 0) qun[warp] = __uint_as_float((unsigned)(127 - 10 + e) << 23) * kKeyUnit;
+        const float f = __uint_as_float((unsigned)(127 + 14 - e) << 23) * (odd ? 0.0625f : 1.f);
+        if (lane == 0) qun[warp] = __uint_as_float((unsigned)(127 - 14 + e) << 23) * kKeyUnit;
         const int kk = 2 * (lane >> 3) + ((lane & 3) >> 1);
         float sh = 0.f, sl = 0.f;
 #pragma unroll
@@ -1200,7 +1205,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const __grid_constan
               vw[u][j][e].y = *reinterpret_cast<const uint32_t*>(vb + (8 * j + 2 * t4 + e) * kRow4 + 4);
             }
             split_f16(p[u][j][0], p[u][j][1], ph[u][j], pl[u][j]);
-            sv[u][j] = vscale[16 * warp + 8 * u + 4 * j + t4];
+            sv[u][j] = lds128(smem_u32(&vscale[16 * warp + 8 * u + 4 * j + t4]));   // in place: 1M rows 356 us otherwise
           }
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {

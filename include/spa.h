@@ -548,7 +548,8 @@ SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int3
  *              1 <= sel_stride <= 2^24
  *   out        device float32 [B][Hq][128]; lse_opt NULL or device float32 [B][Hq]: log2 of the softmax
  *              denominator (-infinity for zeros), as spa_cp_combine takes it
- * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32; the
+ * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32.  4-bit pages whose
+ * value scales, or queries whose 32-dim groups, are too far apart for that (2^16, 2^13) are taken in float32, which is several times slower.  The
  * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes.  Scores (log2 e included) must
  * lie within float32's range (one below it has no weight), and so must the number of attended rows times the largest value. */
 SPA_API spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, const int32_t* block_table,

@@ -198,3 +198,23 @@ def test_values_near_the_end_of_float32(fmt):
     with c:
         out, _ = check(c, q, fmt)
         assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------------------------------------------ queries
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+@pytest.mark.parametrize("e", [10, 16, 24, 40, 60])
+def test_queries_and_keys_of_unequal_groups(fmt, e):
+    """Queries 2^e times larger in one scale group, keys as much smaller there: every group counts alike.  Heads with the large group in
+    different places."""
+    def change(q, k, v):
+        k *= 0.5
+        grp = GK.cuda()
+        for h in range(4):
+            q[0, h, grp == 2] *= 2.0 ** e
+            q[1, h, grp == h] *= 2.0 ** e
+        k[0, :, :, grp == 2] *= 2.0 ** -e
+        k[1, :, :, grp == 0] *= 2.0 ** -e
+        q[1, 1:] *= 2.0 ** -e     # one head sees its large group small, the others theirs at full size
+    q, c = unit_cache(9, 2, 1, 600, fmt, change=change)
+    with c:
+        check(c, q, fmt)
