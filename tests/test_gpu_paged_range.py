@@ -218,3 +218,126 @@ def test_queries_and_keys_of_unequal_groups(fmt, e):
     q, c = unit_cache(9, 2, 1, 600, fmt, change=change)
     with c:
         check(c, q, fmt)
+
+
+# ------------------------------------------------------------------------------------------------ precision
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+@pytest.mark.parametrize("L,Hkv,G", [(257, 8, 4), (5000, 2, 8), (400000, 1, 4)])
+def test_precision_in_the_norm(fmt, L, Hkv, G):
+    """Gaussian rows: the 2-norm of the error over that of the result.  A score's error is a sum of 128 independent roundings
+    of 2^-22 / sqrt(3) of terms of size 1.5 / sqrt(128), 2e-7 to 3e-7 with the tensor cores' own, and so is a weight's, relative; a
+    probability's own rounding and an item's sums add 2^-22 each.  Rows' errors are independent as the values are, so
+    the result's relative error is a row's: 5e-7, and 1e-6 with room.  (Operands of 16 bits and residuals of 8 would give 4e-6, sums left in
+    the tensor cores' accumulators 4e-6 at the longest.)"""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    k, v = torch.randn(2, 1, Hkv, L, 128, generator=g, device="cuda").unbind(0)
+    with Cache([L], Hkv * G, Hkv, fmt, 64, "f32", k=k, v=v) as c:
+        q = 1.5 * torch.randn(1, Hkv * G, 128, generator=g, device="cuda")
+        out, want = check(c, q, fmt)
+        assert float((out.double() - want).norm() / want.norm()) <= 1e-6
+
+
+def test_the_way_a_sequence_is_shared_out_changes_roundings_only():
+    """One sequence alone, and among others of a batch (its rows then split over other CTAs, its pages shared): equal to the
+    sums' roundings."""
+    L, Hkv = 6000, 2
+    g = torch.Generator(device="cuda").manual_seed(12)
+    k, v = torch.randn(2, 1, Hkv, L, 128, generator=g, device="cuda").unbind(0)
+    with Cache([L], 8, Hkv, "int4", 16, "f32", k=k, v=v) as c:
+        q = 1.5 * torch.randn(1, 8, 128, generator=g, device="cuda")
+        want, bound, _, _ = reference(c, q, "int4")
+        one = attend(c, q)
+        n = 100
+        cfg = B.make_paged_config(max_batch=n, n_q_heads=8, n_kv_heads=Hkv, kv_dtype=B.SPA_F32, page_format=B.SPA_PAGE_INT4,
+                                  page_size=16, n_pages=c.pages.numel() // (Hkv * 2304), max_pages=c.table.shape[1])
+        h = B.spa_paged_create(cfg)
+        table = c.table.expand(n, -1).contiguous()
+        lens = i64([L if b % 3 == 0 else b for b in range(n)])
+        many = torch.empty(n, 8, 128, device="cuda")
+        B.spa_attend_paged(h, q.expand(n, -1, -1).contiguous(), c.pages, table, lens, n, 0, many)
+        B.spa_paged_status(h)
+        B.spa_paged_destroy(h)
+        same = many[0::3]
+        assert ((same.double() - want).abs() <= bound).all()
+        rel = float((same - one).double().norm() / (one.double().norm() * math.sqrt(len(same))))
+        assert rel <= 2e-6      # twice the precision of one
+
+
+# ------------------------------------------------------------------------------------------------ the way through float32
+FAR = [
+    # lens, Hq, Hkv, page, heads that see every row (None: all), with lists
+    ([700, 650], 8, 2, 16, None, False),                   # a CTA a slice
+    ([9000], 4, 1, 64, None, False),                       # one slice over many CTAs
+    ([5000, 12000, 1], 24, 8, 48, None, False),            # aligned to slices
+    ([2000] * 20, 16, 8, 128, None, False),                # 160 slices: equal shares, straddling
+    ([40, 1500, 0, 17] * 10, 21, 7, 32, None, False),      # 280 slices of very unequal lengths
+    ([6000, 2500, 0], 16, 4, 16, [1, 0, 0, 1], False),     # sinks and window beside them
+    ([6000, 2500, 90], 16, 4, 32, [1, 0, 1, 1], True),     # lists
+]
+
+
+@pytest.mark.parametrize("case", FAR, ids=lambda c: "%dx%d-%d%s" % (len(c[0]), c[2], max(c[0]), "-lists" if c[5] else "-mask" if c[4] else ""))
+@pytest.mark.parametrize("which", ["rows", "head", "query"])
+def test_far_apart_in_every_share(case, which):
+    """Values or queries that 4 bits take in float32, in every slice or in one, for each way of sharing the work out."""
+    lens, Hq, Hkv, page, mask, listed = case
+    Bs, T, n_sink, window = len(lens), max(lens), 3, 500
+    g = torch.Generator(device="cuda").manual_seed(31)
+    k, v = torch.randn(2, Bs, Hkv, T, 128, generator=g, device="cuda").unbind(0)
+    if which == "rows":
+        v[:, :, 5::37] *= 2.0 ** 20
+        k[:, :, 5::37] *= 0.1
+    if which == "head":
+        v[0, Hkv - 1, :, 40:44] *= 2.0 ** -30
+    with Cache(lens, Hq, Hkv, "int4", page, "f32", k=k, v=v) as c:
+        q = 1.5 * torch.randn(Bs, Hq, 128, generator=g, device="cuda")
+        if which == "query":
+            q[0, 0, GK.cuda() == 1] *= 2.0 ** -20
+        kw, lists = {}, None
+        if mask:
+            kw = dict(head_mask=mask, n_sink=n_sink, window=window)
+        if listed:
+            lists, sel, cnt = {}, torch.full((Bs, Hkv, T), -1, dtype=torch.int32, device="cuda"), torch.zeros(Bs * Hkv, dtype=torch.int32, device="cuda")
+            for b, L in enumerate(lens):
+                for h in range(Hkv):
+                    lo, hi = min(n_sink, L), max(min(n_sink, L), L - window)
+                    lists[b, h] = lo + torch.randperm(hi - lo, generator=g, device="cuda")[:(hi - lo) // 3].sort().values
+                    sel[b, h, :len(lists[b, h])] = lists[b, h].to(torch.int32)
+                    cnt[b * Hkv + h] = len(lists[b, h])
+            kw.update(sel_idx=sel, sel_count=cnt, sel_stride=T)
+        outs = [torch.full((Bs, Hq, 128), float("nan"), device="cuda") for _ in range(2)]
+        lse = torch.full((Bs, Hq), float("nan"), device="cuda")
+        for out in outs:
+            B.spa_attend_paged(c.h, q, c.pages, c.table, c.n, Bs, 0, out, lse=lse, **kw)
+        B.spa_paged_status(c.h)
+        assert torch.equal(*outs)
+        c.check(q, outs[0], lse, mask=mask, n_sink=n_sink if mask else 0, window=window if mask else 0, lists=lists)
+
+
+def test_far_apart_rows_and_bad_pages():
+    """Block table entries and listed positions out of range are skipped there, too, and NaN stays in its scale group."""
+    L = 300
+    g = torch.Generator(device="cuda").manual_seed(32)
+    k, v = torch.randn(2, 1, 1, L, 128, generator=g, device="cuda").unbind(0)
+    v[0, 0, ::7] *= 2.0 ** 25
+    with Cache([L], 4, 1, "int4", 16, "f32", k=k, v=v) as c:
+        q = 1.5 * torch.randn(1, 4, 128, generator=g, device="cuda")
+        t = c.table.clone()
+        t[0, 2], t[0, 9] = -1, 1 << 30
+        out = torch.empty(1, 4, 128, device="cuda")
+        B.spa_attend_paged(c.h, q, c.pages, t, c.n, 1, 0, out)
+        with pytest.raises(B.SpaError):
+            B.spa_paged_status(c.h)
+        rows = torch.tensor([p for p in range(L) if p // 16 not in (2, 9)], device="cuda")
+        c.check(q, out, mask=[1], lists={(0, 0): rows})
+        sel = torch.tensor([[[7, -1, 50, 300, 50, 7 * 16]]], dtype=torch.int32, device="cuda")
+        cnt = torch.tensor([6], dtype=torch.int32, device="cuda")
+        B.spa_attend_paged(c.h, q, c.pages, c.table, c.n, 1, 0, out, head_mask=[1], n_sink=1, window=2, sel_idx=sel, sel_count=cnt, sel_stride=6)
+        with pytest.raises(B.SpaError):
+            B.spa_paged_status(c.h)
+        c.check(q, out, mask=[1], n_sink=1, window=2, lists={(0, 0): torch.tensor([7, 50, 50, 112], device="cuda")})
+    v[0, 0, 77, 4] = float("nan")
+    with Cache([L], 4, 1, "int4", 16, "f32", k=k, v=v) as c:
+        out = attend(c, q)
+        bad = torch.from_numpy(M.GROUP_V == M.GROUP_V[4]).cuda()
+        assert torch.isnan(out[..., bad]).all() and torch.isfinite(out[..., ~bad]).all()
