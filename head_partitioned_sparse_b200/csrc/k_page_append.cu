@@ -622,6 +622,8 @@ __global__ void __launch_bounds__(128) k_page_read(const PagePool P, const ReadA
   }
 }
 
+__global__ void k_clear_bits(unsigned* word, unsigned bits) { atomicAnd(word, ~bits); }
+
 template <typename T, int FMT>
 cudaError_t append_go(const PagePool& pool, const AppendArgs& a, const RopeTab128& tab, unsigned blocks, cudaStream_t st) {
   if (tab.rot == 0) k_page_append<T, FMT, kNone><<<blocks, 128, 0, st>>>(pool, a, tab);
@@ -651,6 +653,11 @@ cudaError_t launch_page_append(const PagePool& pool, AppendArgs a, int dtype, in
                                : append_go<__nv_bfloat16, kPageBf16>(pool, a, tab, (unsigned)blocks, st);
   return format == kPageInt4 ? append_go<float, kPageInt4>(pool, a, tab, (unsigned)blocks, st)
                              : append_go<float, kPageBf16>(pool, a, tab, (unsigned)blocks, st);
+}
+
+cudaError_t launch_clear_bits(unsigned* word, unsigned bits, cudaStream_t st) {
+  k_clear_bits<<<1, 1, 0, st>>>(word, bits);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_page_read(const PagePool& pool, const ReadArgs& a, int dtype, int format, cudaStream_t st) {

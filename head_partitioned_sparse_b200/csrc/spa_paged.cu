@@ -316,7 +316,8 @@ spa_status spa_paged_status(spa_paged* h, spa_stream stream) {
       (e = cudaStreamSynchronize(st)) != cudaSuccess)
     return cuda_fail(e, "spa_paged_status");
   if (w == 0) return SPA_OK;
-  if ((e = cudaMemsetAsync(h->err, 0, 4, st)) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
+  // Only what was read: appends and reads of other streams may have set more since.
+  if ((e = spa::launch_clear_bits(h->err, w, st)) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
     return cuda_fail(e, "spa_paged_status");
   if (w & spa::kErrTimeout) return fail(SPA_ERR_DEVICE_TIMEOUT, "a copy into shared memory did not arrive in time; outputs are not valid");
   return fail(SPA_ERR_DEVICE_RANGE, "out of range on the device:%s%s%s%s", w & spa::kErrSeqLen ? " a length (clamped);" : "",

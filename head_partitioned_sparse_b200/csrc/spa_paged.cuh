@@ -115,6 +115,7 @@ cudaError_t launch_rope(const void* x, void* y, Strides3 xs, Strides3 ys, const 
 cudaError_t launch_page_append(const PagePool& pool, AppendArgs a, int dtype, int format, const RopeTab128& tab,
                                int num_sms, cudaStream_t st);
 cudaError_t launch_page_read(const PagePool& pool, const ReadArgs& a, int dtype, int format, cudaStream_t st);
+cudaError_t launch_clear_bits(unsigned* word, unsigned bits, cudaStream_t st);
 int page_attend_setup(int format);   // 0: the kernel cannot be resident
 cudaError_t launch_page_attend(const PagedAttendArgs& a, int format, int grid, const RopeTab128& tab, cudaStream_t st);
 

@@ -508,8 +508,8 @@ SPA_API spa_status spa_paged_page_bytes(const spa_paged_config* cfg, size_t* byt
 SPA_API spa_status spa_paged_create(spa_paged** out, const spa_paged_config* cfg, const spa_rope* rope);
 /* Frees the workspace (synchronises the device first).  NULL is accepted. */
 SPA_API spa_status spa_paged_destroy(spa_paged* h);
-/* Synchronises `stream`, reads and clears the status word: SPA_OK, SPA_ERR_DEVICE_RANGE or
- * SPA_ERR_DEVICE_TIMEOUT. */
+/* Synchronises `stream`, reads the status word and clears what it read: SPA_OK, SPA_ERR_DEVICE_RANGE or
+ * SPA_ERR_DEVICE_TIMEOUT.  What calls on other streams set meanwhile is left for the next one. */
 SPA_API spa_status spa_paged_status(spa_paged* h, spa_stream stream);
 
 /* Rotates, rounds and stores T new tokens of every (sequence, KV head) at positions
