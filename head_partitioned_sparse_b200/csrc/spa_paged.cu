@@ -120,6 +120,14 @@ PagedPlan plan(const spa_paged_config& c, int grid) {
   return p;
 }
 
+spa_status check_device(const spa_paged* h) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev != h->device)
+    return fail(SPA_ERR_INVALID_ARG, "the handle was created on device %d, the current device is %d", h->device, dev);
+  return SPA_OK;
+}
 // Checks that every call on a paged cache shares.
 spa_status check_call(const spa_paged* h, const void* pages, const int32_t* block_table, int B) {
   if (!h) return fail(SPA_ERR_INVALID_ARG, "handle is NULL");
@@ -128,12 +136,7 @@ spa_status check_call(const spa_paged* h, const void* pages, const int32_t* bloc
     return fail(SPA_ERR_INVALID_ARG, "pages must be 16-byte aligned, block_table 4-byte aligned");
   if (B < 1 || B > h->cfg.max_batch)
     return fail(SPA_ERR_INVALID_ARG, "B must be in [1, max_batch=%d] (got %d)", h->cfg.max_batch, B);
-  int dev = -1;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (dev != h->device)
-    return fail(SPA_ERR_INVALID_ARG, "the handle was created on device %d, the current device is %d", h->device, dev);
-  return SPA_OK;
+  return check_device(h);
 }
 spa::PagePool pool_of(const spa_paged* h, const void* pages, const int32_t* table) {
   const spa_paged_config& c = h->cfg;
@@ -309,6 +312,8 @@ spa_status spa_paged_destroy(spa_paged* h) {
 
 spa_status spa_paged_status(spa_paged* h, spa_stream stream) {
   if (!h) return fail(SPA_ERR_INVALID_ARG, "handle is NULL");
+  const spa_status r = check_device(h);
+  if (r) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   unsigned w = 0;
   cudaError_t e;

@@ -55,3 +55,13 @@ def test_status_keeps_what_was_set_after_it_was_read(lib, handle):
     assert lib.spa_paged_status(handle, None) == B.SPA_ERR_DEVICE_RANGE
     assert b"block_table" in lib.fake_last_error() and b"position" not in lib.fake_last_error()
     assert lib.spa_paged_status(handle, None) == B.SPA_OK
+
+
+def test_status_needs_the_handles_device(lib, handle):
+    append(lib, handle)
+    var(lib, "fake_device").value = 1
+    assert lib.spa_paged_status(handle, None) == B.SPA_ERR_INVALID_ARG
+    assert b"device" in lib.fake_last_error()
+    var(lib, "fake_device").value = 0
+    assert lib.spa_paged_status(handle, None) == B.SPA_ERR_DEVICE_RANGE
+    assert lib.spa_paged_status(handle, None) == B.SPA_OK
