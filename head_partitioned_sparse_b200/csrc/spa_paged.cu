@@ -303,8 +303,12 @@ spa_status spa_paged_create(spa_paged** out, const spa_paged_config* cfg, const 
 
 spa_status spa_paged_destroy(spa_paged* h) {
   if (!h) return SPA_OK;
+  int dev = h->device;
+  cudaGetDevice(&dev);
+  if (dev != h->device) cudaSetDevice(h->device);
   cudaDeviceSynchronize();
   const cudaError_t e = cudaFree(h->mem);
+  if (dev != h->device) cudaSetDevice(dev);
   delete h;
   if (e != cudaSuccess) return cuda_fail(e, "cudaFree");
   return SPA_OK;

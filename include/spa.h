@@ -506,7 +506,7 @@ SPA_API spa_status spa_paged_page_bytes(const spa_paged_config* cfg, size_t* byt
 /* `rope` turns the appended keys and the queries (rot_dim <= 128); its table is copied.  NULL: no
  * rotation (both come rotated).  Synchronous.  On failure *out is NULL. */
 SPA_API spa_status spa_paged_create(spa_paged** out, const spa_paged_config* cfg, const spa_rope* rope);
-/* Frees the workspace (synchronises the device first).  NULL is accepted. */
+/* Frees the workspace (synchronises the handle's device first, whichever is current).  NULL is accepted. */
 SPA_API spa_status spa_paged_destroy(spa_paged* h);
 /* Synchronises `stream`, reads the status word and clears what it read: SPA_OK, SPA_ERR_DEVICE_RANGE or
  * SPA_ERR_DEVICE_TIMEOUT.  What calls on other streams set meanwhile is left for the next one. */

@@ -65,3 +65,12 @@ def test_status_needs_the_handles_device(lib, handle):
     var(lib, "fake_device").value = 0
     assert lib.spa_paged_status(handle, None) == B.SPA_ERR_DEVICE_RANGE
     assert lib.spa_paged_status(handle, None) == B.SPA_OK
+
+
+def test_destroy_waits_for_the_handles_device(lib, handle):
+    var(lib, "fake_device").value = 1
+    var(lib, "fake_synced_on").value = var(lib, "fake_freed_on").value = -1
+    assert lib.spa_paged_destroy(handle) == B.SPA_OK
+    handle.value = None
+    assert var(lib, "fake_synced_on").value == 0 and var(lib, "fake_freed_on").value == 0
+    assert var(lib, "fake_device").value == 1
