@@ -14,8 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 @pytest.fixture(scope="module")
 def lib(tmp_path_factory):
     so = tmp_path_factory.mktemp("fake") / "libfake.so"
+    # -Bsymbolic: its own runtime, also where torch has loaded the real one
     subprocess.run([build._nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O1", "-std=c++17", "--shared", "-cudart", "none",
-                    "-Xcompiler", "-fPIC", "-I", build.CSRC, "-I", os.path.join(build.ROOT, "include"), "-o", str(so),
+                    "-Xcompiler", "-fPIC", "-Xlinker", "-Bsymbolic", "-I", build.CSRC, "-I", os.path.join(build.ROOT, "include"), "-o", str(so),
                     os.path.join(build.CSRC, "spa_paged.cu"), os.path.join(HERE, "fake_paged_launches.cu"), os.path.join(HERE, "fake_cuda_runtime.cpp")], check=True)
     lib = ctypes.CDLL(str(so))
     for name in ("spa_paged_create", "spa_paged_destroy", "spa_paged_status", "spa_kv_append_paged"):
