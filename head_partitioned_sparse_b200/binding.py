@@ -460,6 +460,8 @@ def _on(s, device: int) -> Optional[int]:
 
 @functools.lru_cache(maxsize=256)
 def _stride_array(s):
+    if len(s) != 3:
+        raise ValueError(f"expected the strides of (batch, token, head), got {s}")
     return (ctypes.c_int64 * 3)(*s)
 
 

@@ -129,3 +129,16 @@ def test_model_pool_round_trip(fmt):
             # half a step of a group's scale: amax / 14, the scale itself off by 2^-9, the top level by as much
             amax = np.array([np.abs(x[grp == g2]).max() for g2 in range(4)])[grp]
             assert (np.abs(y - x) <= amax / 14 * (1 + 2.0 ** -8) + amax * 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 4])
+def test_strides_of_another_length_are_refused(rope, n):
+    """Two strides would leave every head at the same place."""
+    X, s = 0x10000, (64,) * n
+    for kw in (dict(x_strides=s), dict(y_strides=s)):
+        with pytest.raises(ValueError, match="strides"):
+            B.spa_rope_apply(rope, X, X, 1, 1, 1, 64, B.SPA_BF16, start_pos=X, **kw)
+    for f in (B.spa_kv_append_paged, B.spa_kv_read_paged):
+        for kw in (dict(k_strides=s), dict(v_strides=s)):
+            with pytest.raises(ValueError, match="strides"):
+                f(None, X, X, X, 1, 1, X, X, **kw)
