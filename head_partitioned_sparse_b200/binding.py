@@ -433,7 +433,10 @@ def _device() -> int:
         if not torch.cuda.is_available():
             return -1
         torch.cuda.init()
-        _torch_cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        # torch's own short ways, and the public functions where a release does not have them
+        _torch_cuda = (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+                       getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda device: torch.cuda.current_stream(device).cuda_stream))
     return _torch_cuda[0]()
 
 

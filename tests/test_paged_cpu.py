@@ -142,3 +142,22 @@ def test_strides_of_another_length_are_refused(rope, n):
         for kw in (dict(k_strides=s), dict(v_strides=s)):
             with pytest.raises(ValueError, match="strides"):
                 f(None, X, X, X, 1, 1, X, X, **kw)
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_device_and_stream_without_torchs_private_functions(monkeypatch, private):
+    class Stream:
+        cuda_stream = 0x77
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream() if device == 1 else None)
+    if private:
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x77, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(B, "_torch_cuda", None)
+    assert B._device() == 1
+    assert B._on(None, 1) == 0x77 and B._on(0x55, 1) == 0x55 and B._on(Stream(), 1) == 0x77
