@@ -1,5 +1,10 @@
 """Rotary and paged-cache entry points: what is refused on the host, before any GPU is touched, and the
 float64 model's own consistency.  No compute calls here."""
+import ctypes
+import os
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -161,3 +166,20 @@ def test_device_and_stream_without_torchs_private_functions(monkeypatch, private
     monkeypatch.setattr(B, "_torch_cuda", None)
     assert B._device() == 1
     assert B._on(None, 1) == 0x77 and B._on(0x55, 1) == 0x55 and B._on(Stream(), 1) == 0x77
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
+@pytest.mark.parametrize("name", ["spa_rope_config", "spa_paged_config"])
+def test_config_layouts_match_the_header(tmp_path, name):
+    """The ctypes mirrors have the C layout (size and every field offset)."""
+    mirror = getattr(B, name)
+    fields = [f for f, _ in mirror._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "spa.h"\nint main(void) {\n'
+                   f'  printf("%zu", sizeof({name}));\n'
+                   + "".join(f'  printf(" %zu", offsetof({name}, {f}));\n' for f in fields) + "  return 0;\n}\n")
+    exe = tmp_path / "layout"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert got == [ctypes.sizeof(mirror)] + [getattr(mirror, f).offset for f in fields]
