@@ -47,6 +47,7 @@ spa_status fill_table(const spa_rope_config& c, spa::RopeTabAny* t) {
   const int n = c.rot_dim / 2;
   double theta = c.theta;
   if (c.scaling == SPA_ROPE_BASE) theta *= std::pow(c.factor, (double)c.rot_dim / (c.rot_dim - 2));
+  if (!std::isfinite(theta)) return fail(SPA_ERR_INVALID_ARG, "theta * factor^(rot_dim / (rot_dim - 2)) is not finite");
   double first = 0, last = 0;
   if (c.scaling == SPA_ROPE_RAMP) {
     auto dim = [&](double turns) { return c.rot_dim * std::log((double)c.orig_ctx / (2 * kPi * turns)) / (2 * std::log(theta)); };

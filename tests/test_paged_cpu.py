@@ -183,3 +183,13 @@ def test_config_layouts_match_the_header(tmp_path, name):
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(mirror)] + [getattr(mirror, f).offset for f in fields]
+
+
+def test_a_base_that_overflows_is_refused():
+    """theta * factor^(rot_dim / (rot_dim - 2)) past 64 bits would leave every frequency but the first at 0."""
+    ok = dict(scaling=B.SPA_ROPE_BASE, theta=1e4)
+    r = B.spa_rope_create(B.make_rope_config(**ok, factor=1e290))
+    f = np.array(B.spa_rope_inv_freq(r, 64))
+    assert np.allclose(f, M.frequencies(128, theta=1e4, scaling="base", factor=1e290), rtol=1e-12, atol=0) and (f > 0).all()
+    B.spa_rope_destroy(r)
+    refused(B.SPA_ERR_INVALID_ARG, B.spa_rope_create, B.make_rope_config(**ok, factor=1e305))
