@@ -550,7 +550,8 @@ SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int3
  *              denominator (-infinity for zeros), as spa_cp_combine takes it
  * Queries and probabilities are kept to 22 bits (24 over bf16 pages) for the tensor cores, sums in float32.  4-bit pages whose
  * value scales, or queries whose 32-dim groups, are too far apart for that (2^16, 2^13) are taken in float32, which is several times slower.  The
- * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes.  Scores (log2 e included) must
+ * result does not depend on timing.  Masked rows contribute nothing, whatever their bytes; an infinity or NaN in a query or an attended row
+ * leaves the outputs that it reaches undefined (NaN as a rule).  Scores (log2 e included) must
  * lie within float32's range (one below it has no weight), and so must the number of attended rows times the largest value. */
 SPA_API spa_status spa_attend_paged(spa_paged* h, const void* q_pre, const void* pages, const int32_t* block_table,
                       const int64_t* seq_lens, int B, int64_t max_seq_len, const uint8_t* head_mask_opt, int n_sink,
