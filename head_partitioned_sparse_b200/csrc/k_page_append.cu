@@ -17,8 +17,10 @@
 // a rotated key within the rotation's error of a border (about 1 row in 500 by the bounds used), a float32 row near one and a group
 // that is tiny or not finite take a second, exact way: products of few bits, and 64 bits for the rotation.
 //
-// A row pair moves 512 + 144 bytes at bf16, so memory would bound it; the exact rounding's instructions do: 32K
-// tokens of 8 heads take 51 us (3.4 TB/s, 67 % of the issue slots) where a copy of the bytes takes 26.  Into bf16
+// A row pair moves 512 + 144 bytes at bf16, so memory would bound it; the exact rounding does, by its instructions and the waits
+// between them: 32K tokens of 8 heads take 51 us (3.4 TB/s) where a copy of the bytes takes 26 and the 247 instructions
+// of two row pairs 28 at full issue (67 % of the slots are filled, by 16 warps an SM of 124 registers).  In float32 rows the append and the
+// read of them take 138 us for 93 of bytes.  Into bf16
 // pages, without them, that append and the read of its rows run at 0.9 of the copy rate (91 us, 537 MB).  8 lanes own the K and V rows of one (token, head),
 // lane e the dims 8 e .. 8 e + 7 and 64 further of both: the pairs of a whole-head rotation meet in one lane, its 16
 // dims are of one scale group of K and of two of V (group maxima in 1 and 2 shuffles), and every
@@ -28,11 +30,6 @@
 namespace spa {
 namespace {
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // 8 dims of a row as loaded.  top(): float bits of the largest magnitude, NaN above infinity.
 template <typename T>
 struct Dims;

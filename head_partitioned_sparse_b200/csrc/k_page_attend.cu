@@ -20,11 +20,12 @@
 //
 // Matrix mapping (mma.sync m16n8k16, float32 sums).  The 16 rows of the operand hold the group's heads more
 // than once, as a high part and residuals, so that no bits of queries and probabilities are lost:
-//   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought
-//     to a maximum of 2^14 a head (the largest of every scale group then keeps 22 bits down to 2^-13 of that); probabilities are 2^14 times their value at most and value scales below 2
-//     by the largest scale the warp has met (a power of two, moved like the running maximum), so float16's
-//     range holds both, and the products that count keep 22 bits, while the scales met lie within 2^16 of each other.  Where
-//     scales or queries lie farther apart, the CTA takes its piece of the slice once more at the end, in float32 (attend_wide).  A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
+//   4 bits: float16 high parts (rows 0-7) and residuals (rows 8-15), 22 bits.  Queries are brought to a maximum of
+//     2^14 a head; a scale group whose own maximum is 2^-13 of that still keeps 22 bits.  Probabilities are 2^14 times
+//     their value at most, and value scales below 2 by the largest scale the warp has met (a power of two, moved like the
+//     running maximum); the products that count keep 22 bits while the scales met lie within 2^16 of each other.  Where queries
+//     or scales lie farther apart, the CTA takes its piece of the slice once more at the end, in float32 (attend_wide).
+//     A code word (8 nibbles) becomes four float16 pairs, (nibble j, nibble j + 4).
 //     Scores: word w of a lane's 16 bytes is scale group w of its 32 dims, so the products of a group
 //     are summed by themselves (starting at -8 times the sum of the queries, which centres
 //     the codes) and scaled once a (row, group), not once an element.
@@ -191,11 +192,6 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
   y -= bf16_hi(hi);
   mid = pack2(x, y);
   lo = pack2(x - bf16_lo(mid), y - bf16_hi(mid));
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 // 4 bits: probabilities are 2^14 times their value (less where scores' steps are coarser), value scales in float16 below 2.  A
 // probability in two float16 parts is off by 2^-25 at most where its leading bits run out, against 2^14 of the row with the
@@ -681,14 +677,18 @@ __global__ void __launch_bounds__(W * 32, 1) k_attend_paged(const __grid_constan
     for (int i = tid; i < G * kHeadDim; i += W * 32) A.out[h0 * kHeadDim + i] = 0.f;
     if (A.lse && tid < G) A.lse[h0 + tid] = -INFINITY;
   }
-  // ---- shares.  A CTA a slice where those are small and few.  Else aligned to slices: a slice of n items takes
-  // ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice; taken where its
-  // largest share exceeds the equal one by no more than the slices passed through would cost a CTA: kPieceItems for a second,
-  // as much again where some slice is shorter than a share (a CTA then meets three).  Over bf16 pages, where memory bounds the
-  // call and a few idle CTAs cost little, by 0.3 of it too.  Else equal shares, down to one item a CTA.  us with equal shares against aligned ones: one sequence of 4096 rows 19.4 /
-  // 14.1, 16 of them 37.4 / 32.7, 4 x 128K with lists 55.2 / 51.6, 3 x 128K with half of the heads streaming 80.7 / 75.8; but 1M rows
-  // of 8 heads 344 / 348, and 16 x 64K of bf16, a quarter of the heads seeing every row, 134 / 429.  5 x 64K of those
-  // with a limit of 24 items, 0.3, 0.6: 64.7 / 60.4 / 60.4; 9 x 128K with lists, 4 bits: 83.7 / 83.7 / 94.4.
+  // ---- shares: a CTA a slice where the slices are small and few; else aligned to slices or equal.
+  // Aligned: a slice of n items takes ceil(n / most) CTAs, with `most` the least (but an item a warp) for which the CTAs suffice.
+  // A CTA then has one slice's queries and merge, at the price of a largest share above the equal one.  Taken where that
+  // price is no more than the slices that an equal share passes through: kPieceItems for a second, as much again where some
+  // slice is shorter than a share (a CTA then meets three).  Over bf16 pages, where memory bounds the call and
+  // a few idle CTAs cost little, kUneven of a share is accepted too.
+  // Equal: down to one item a CTA.
+  // us, equal against aligned: one sequence of 4096 rows 19.4 / 14.1, 16 of them 37.4 / 32.7, 4 x 128K with lists 55.2 / 51.6,
+  // 3 x 128K with half of the heads streaming 80.7 / 75.8; but 1M rows of 8 heads 344 / 348, and 16 x 64K of bf16, a
+  // quarter of the heads seeing every row, 134 / 429.
+  // us, bf16 of 64K with kUneven at 0, 0.3, 0.6: 5 sequences, a quarter of the heads seeing every row, 64.7 / 60.4 / 60.4;
+  // 7 of them - / 82.5 / 76.4; 8 - / 86.6 / 84.8; 10, half of the heads, - / 171.4 / 179.
   constexpr int kLaneSlices = 5, kPieceItems = 24;
   constexpr float kUneven = 0.3f;
   if (!small) {

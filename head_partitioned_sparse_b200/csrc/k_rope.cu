@@ -4,11 +4,12 @@
 // gradient of x is the transposed map m R(pos)^T dy: the same kernel with sin a negated.
 //
 // Bound by memory: 2 elements moved for 3 flops (32K tokens of 40 heads in bf16: 671 MB in 102 us, 6.6 TB/s, the rate of
-// a plain copy; 8-byte chunks of 36 of 80 dims in float32: 47 MB in 12.9 us, 3.7 TB/s).  A thread owns one chunk of pairs of one
+// a plain copy; 36 of 80 dims in float32, where one chunk width serves the whole row and 18 pairs allow 8 bytes: 47 MB
+// in 12.7 us, 3.7 TB/s).  A thread owns one chunk of pairs of one
 // token (16 bytes of each half, or 16 bytes of interleaved pairs), takes the cosines and
 // sines of its pairs once and applies them to several heads, so the 64-bit angle and the
 // sincos are paid once for up to kHeads rows.  The table travels with the launch, so it belongs to no
-// device; its 128 pairs cost a small call no more than 64 would (5.7 against 5.8 us of the host, 2.8 of the GPU).
+// device; its 256 pairs cost a small call no more than 128 or 64 would (5.3 to 5.7 us of the host and 2.74 of the GPU with each).
 #include "spa_paged.cuh"
 
 namespace spa {

@@ -19,6 +19,12 @@ constexpr int kMergeWords = 9 * 32 * 4;             // a warp's or CTA's attenti
 constexpr unsigned kErrPage = 16u;    // block_table entry outside [0, n_pages)
 constexpr unsigned kErrList = 32u;    // selected count or position out of range
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Rotation of a head's first rot dims.  f_pi: effective inverse frequencies / pi.  Passed to
 // kernels by value, so that a table belongs to no device and a captured graph keeps its own.
 template <int N>

@@ -528,7 +528,8 @@ SPA_API spa_status spa_kv_append_paged(spa_paged* h, const void* k_pre, const in
 /* Reads positions start_pos[b] + t, t < n_rows[b] (NULL: T), as stored: rotated keys, and for
  * SPA_PAGE_INT4 the values that the codes stand for, rounded to kv_dtype.  Into k_rows, v_rows
  * [B][T][n_kv_heads][128] by HOST strides, as for the append (NULL: dense [B][n_kv_heads][T][128], which
- * spa_prefill and spa_decode take as a cache of T rows when start_pos is 0).  Rows at and behind n_rows[b], and
+ * spa_prefill and spa_decode take as a cache of T rows when start_pos is 0; they rotate their queries by SPA_ROPE_PLAIN,
+ * SPA_ROPE_HALF, rot_dim 128, magnitude 1 and their own rope_theta, so the keys have to be rotated that way).  Rows at and behind n_rows[b], and
  * rows whose position or page is out of range, are left as they were. */
 SPA_API spa_status spa_kv_read_paged(spa_paged* h, const void* pages, const int32_t* block_table,
                       const int64_t* start_pos, const int64_t* n_rows_opt, int B, int T, void* k_rows,
