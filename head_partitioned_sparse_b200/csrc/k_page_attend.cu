@@ -383,12 +383,11 @@ __device__ __forceinline__ void centred(unsigned w, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x4b000000u | (w >> (4 * i) & 15u)) - 8388616.f;
 }
-// A CTA's piece of a slice of 4-bit pages in float32 throughout, for rows whose value scales, or queries whose scale groups, are too far apart
-// for float16 products.  The
-// queries are in qs; `unit` is the piece's first unit of the slice, `items` the number of its items, which the warps take in turn.  A lane
-// scores one row of an item for every head, then sums 4 dims over the rows.  Leaves the states in mbuf as the kernel's own
-// hand-over does.  One row of 1M, 8 KV heads of 8 queries: 2.2 ms in place of 0.37 (one CTA takes 57000 rows again); of 64K, 170 us
-// in place of 50.  Loads of queries and shuffles bound it.
+// A CTA's piece of a slice of 4-bit pages in float32 throughout, for value scales, or scale groups of a query, that are too far
+// apart for float16 products.  The queries are in qs; `unit` is the piece's first unit of the slice, `items` the number of its
+// items, which the warps take in turn.  A lane scores one row of an item for every head, then sums 4 dims over the rows.
+// Leaves the states in mbuf as the kernel's own hand-over does.  One such row among 1M, 8 KV heads of 8 queries: 2.2 ms in
+// place of 0.37 (one CTA takes 57000 rows again); among 64K, 170 us in place of 50.  Loads of queries and shuffles bound it.
 template <int W, int U>
 __device__ __forceinline__ void attend_wide(const PagedAttendArgs& A, const Slice& S, const float* qs, float* mbuf, int s, int unit, int items) {
   static_assert(U == 2, "a lane a row of an item");
@@ -535,7 +534,7 @@ __device__ __forceinline__ void attend_wide(const PagedAttendArgs& A, const Slic
   __syncthreads();
 }
 
-// The CTAs that share slice s, whose items are [lo, hi).  split: see s_split.
+// The CTAs that share a slice whose items are [lo, hi).  split: see s_split.
 __device__ __forceinline__ void owners(const int4& split, int nb, long long T, long long lo, long long hi, int& c0, int& c1) {
   const bool aligned = split.z >= 0;
   c0 = aligned ? split.y : (int)(((lo + 1) * nb - 1) / T);
